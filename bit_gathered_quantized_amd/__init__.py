@@ -11,10 +11,13 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
+from .layer import MoeNorm, block_norm
+
 __all__ = [
     "MoeError", "lib", "LIB_PATH", "MOE_F_FP32_OUT", "MOE_F_FP32_INTERMEDIATE", "MOE_F_SWIGLU",
     "max_tiles", "workspace_bytes", "workspace_layout", "sort_build_tiles",
     "expert_ffn_forward", "router_topk", "status_string", "EXPORTED_SYMBOLS",
+    "block_norm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoeffn.so")
@@ -33,7 +36,7 @@ EXPORTED_SYMBOLS = (
     "moe_max_tiles", "moe_sort_build_tiles", "moe_ffn_workspace_bytes",
     "moe_ffn_workspace_layout", "moe_expert_ffn_forward",
     "moe_expert_ffn_forward_timed", "moe_expert_ffn_forward_presorted", "moe_router_topk",
-    "moe_status_string", "moe_expert_ffn_forward_noalloc",
+    "moe_status_string", "moe_expert_ffn_forward_noalloc", "moe_block_norm",
 )
 MOE_ERR_SCRATCH = -7
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -93,6 +96,8 @@ def lib():
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_router_topk.argtypes = [P, i32, i32, i32, P, P, P]
         L.moe_router_topk.restype = i32
+        L.moe_block_norm.argtypes = [ctypes.POINTER(MoeNorm), P, P]
+        L.moe_block_norm.restype = i32
         _lib = L
     return _lib
 

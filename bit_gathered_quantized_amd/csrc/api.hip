@@ -221,9 +221,74 @@ moe_status forward_impl(const moe_problem* p, const void* x, const int32_t* ids,
     return MOE_OK;
 }
 
+bool known_type(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP32; }
+size_t type_size(int32_t t) { return t == MOE_T_FP32 ? 4 : 2; }
+
+// The checks of a block norm apart from y's pointer (y_stride is checked).
+moe_status check_norm(const moe_norm* n) {
+    if (!n) return MOE_ERR_NULL;
+    if (!known_type(n->y_type) || !known_type(n->stream_type) || !known_type(n->normed_type) ||
+        !known_type(n->weight_type) || !known_type(n->gate_type) || (n->flags & ~MOE_N_POST))
+        return MOE_ERR_UNSUPPORTED;
+    if (n->T < 0 || n->H < 1) return MOE_ERR_SHAPE;
+    if (n->H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
+    if (!(n->eps >= 0.f)) return MOE_ERR_SHAPE;
+    if (n->T == 0) return MOE_OK;
+    if (!n->out && !n->normed) return MOE_ERR_NULL;
+    if (n->y_stride < 0 || (n->residual && n->residual_stride < 0) || (n->out && n->out_stride < n->H) ||
+        (n->normed && n->normed_stride < n->H))
+        return MOE_ERR_SHAPE;
+    if (n->gate && (n->gate_stride_t < 0 || n->gate_stride_h < 0 || n->gate_stride_h > 1)) return MOE_ERR_SHAPE;
+    const size_t ws = type_size(n->weight_type), ss = type_size(n->stream_type);
+    if (!aligned(n->residual, ss) || !aligned(n->out, ss) || !aligned(n->normed, type_size(n->normed_type)) ||
+        !aligned(n->post_weight, ws) || !aligned(n->pre_weight, ws) || !aligned(n->gate, type_size(n->gate_type)))
+        return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+moe::NormArgs norm_args(const moe_norm* n, const void* y) {
+    moe::NormArgs a = {};
+    a.T = n->T;
+    a.H = n->H;
+    a.post = n->flags & MOE_N_POST;
+    a.y_f32 = n->y_type == MOE_T_FP32;
+    a.stream_f32 = n->stream_type == MOE_T_FP32;
+    a.normed_f32 = n->normed_type == MOE_T_FP32;
+    a.weight_f32 = n->weight_type == MOE_T_FP32;
+    a.gate_f32 = n->gate_type == MOE_T_FP32;
+    a.eps = n->eps;
+    a.residual_scale = n->residual_scale;
+    a.gate_scale = n->gate_scale;
+    a.weight_offset = n->weight_offset;
+    a.y = y;
+    a.residual = n->residual;
+    a.post_weight = a.post ? n->post_weight : nullptr;
+    a.gate = n->gate;
+    a.pre_weight = n->normed ? n->pre_weight : nullptr;
+    a.out = n->out;
+    a.normed = n->normed;
+    a.y_stride = n->y_stride;
+    a.residual_stride = n->residual ? n->residual_stride : 0;
+    a.out_stride = n->out ? n->out_stride : 0;
+    a.normed_stride = n->normed ? n->normed_stride : 0;
+    a.gate_stride_t = n->gate ? n->gate_stride_t : 0;
+    a.gate_stride_h = n->gate ? n->gate_stride_h : 0;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream) {
+    const moe_status st = check_norm(n);
+    if (st != MOE_OK) return st;
+    if (n->T == 0) return MOE_OK;
+    if (!y) return MOE_ERR_NULL;
+    if (!aligned(y, type_size(n->y_type))) return MOE_ERR_ALIGN;
+    const hipError_t e = moe::launch_block_norm(norm_args(n, y), static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
 
 int32_t moe_max_tiles(int64_t A, int32_t E, int32_t bm_big) {
     if (A < 0 || E < 1 || bm_big < 1) return -1;

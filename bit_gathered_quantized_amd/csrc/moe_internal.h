@@ -284,4 +284,18 @@ hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t
                               float* weights, hipStream_t stream);
 constexpr int kRouterMaxK = 64;
 
+// The block norm (norm.hip).  Types as booleans (fp32, else bf16).
+struct NormArgs {
+    int32_t T, H;
+    bool post, y_f32, stream_f32, normed_f32, weight_f32, gate_f32;
+    float eps, residual_scale, gate_scale, weight_offset;
+    const void *y, *residual, *post_weight, *gate, *pre_weight;
+    void *out, *normed;
+    int64_t y_stride, residual_stride, out_stride, normed_stride, gate_stride_t, gate_stride_h;
+    // y as the down matmul's slots (ids != nullptr): fp32 [T * k, H], see norm.hip
+    const int32_t* ids;
+    int32_t k, E;
+};
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,198 @@
+"""Binding of the operators around the expert FFN: the block norms.
+
+As in the package itself, argument checks and marshalling only; the work runs
+in the HIP kernels of ``libmoeffn.so`` and PyTorch supplies memory and streams.
+Everything is enqueued on ``stream`` (default: the current stream of the
+tensors' device); outputs that the caller does not give are allocated for that
+stream.
+"""
+
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+__all__ = ["MoeNorm", "block_norm", "MOE_T_BF16", "MOE_T_FP32", "MOE_N_POST", "NORM_MAX_H"]
+
+MOE_T_BF16, MOE_T_FP32 = 0, 1
+MOE_N_POST = 1
+NORM_MAX_H = 16384
+
+
+class MoeNorm(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("T", "H", "y_type", "stream_type", "normed_type", "weight_type", "gate_type")] + \
+               [("flags", ctypes.c_uint32)] + \
+               [(n, ctypes.c_float) for n in ("eps", "residual_scale", "gate_scale", "weight_offset")] + \
+               [(n, ctypes.c_void_p) for n in
+                ("residual", "post_weight", "gate", "pre_weight", "out", "normed")] + \
+               [(n, ctypes.c_int64) for n in
+                ("y_stride", "residual_stride", "out_stride", "normed_stride", "gate_stride_t", "gate_stride_h")]
+
+
+def _api():
+    """The package (imported late: it imports this module)."""
+    import bit_gathered_quantized_amd as bgq
+    return bgq
+
+
+def _type(t, name):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MOE_T_BF16
+    if t.dtype is torch.float32:
+        return MOE_T_FP32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _on(t, name, dev):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _device(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    return t.device
+
+
+def _rows(t, name, dev, T, H):
+    """Row stride of a [T, H] tensor whose rows are contiguous."""
+    _on(t, name, dev)
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H)}")
+    if t.stride(1) != 1 and H > 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    return t.stride(0) if T > 1 else max(H, 1)
+
+
+def _vector(t, name, dev, n):
+    _on(t, name, dev)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+@contextlib.contextmanager
+def _ambient(dev, stream):
+    """Makes the tensors' device, and the stream if one is given, current."""
+    import torch
+    with contextlib.ExitStack() as stack:
+        if dev.index != torch.cuda.current_device():
+            stack.enter_context(torch.cuda.device(dev))
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream belongs to {stream.device}, the tensors are on {dev}")
+            stack.enter_context(torch.cuda.stream(stream))
+        yield
+
+
+def _call(dev, stream, f):
+    """f(raw stream) with the device and stream current; no context in the usual case."""
+    import torch
+    if stream is None and dev.index == torch.cuda.current_device():
+        return f(torch.cuda.current_stream(dev).cuda_stream)
+    with _ambient(dev, stream):
+        return f(torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_scale, pre_norm, pre_weight,
+               weight_offset, eps):
+    """Fills everything of a MoeNorm but its outputs and y; returns the normed flag."""
+    n.T, n.H, n.eps, n.residual_scale, n.weight_offset = T, H, eps, residual_scale, weight_offset
+    n.gate_scale = 1.0
+    if residual is not None:
+        n.stream_type = _type(residual, "residual")
+        n.residual_stride = _rows(residual, "residual", dev, T, H)
+        n.residual = residual.data_ptr()
+    if post_norm or post_weight is not None:
+        n.flags = MOE_N_POST
+    for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if w is not None:
+            n.weight_type = _type(w, name)
+            setattr(n, name, _vector(w, name, dev, H))
+    if post_weight is not None and pre_weight is not None and post_weight.dtype != pre_weight.dtype:
+        raise ValueError("post_weight and pre_weight must have the same type")
+    if gate is not None:
+        if isinstance(gate, (int, float)):
+            n.gate_scale = gate
+        else:
+            _on(gate, "gate", dev)
+            n.gate_type = _type(gate, "gate")
+            try:
+                g = gate.expand(T, H)
+            except RuntimeError:
+                raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}") from None
+            st, sh = g.stride()
+            if H == 1:
+                sh = 0
+            if sh not in (0, 1):
+                raise ValueError("gate must be contiguous or broadcast along H")
+            n.gate, n.gate_stride_t, n.gate_stride_h = g.data_ptr(), st if T > 1 else 0, sh
+    return pre_norm or pre_weight is not None
+
+
+def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None, residual_scale=1.0,
+               pre_norm=False, pre_weight=None, weight_offset=0.0, eps=1e-6, out=None, normed=None, want_out=True,
+               stream=None):
+    """Norms around a block, fused with its gate and the residual scale, in one pass:
+
+        z      = gate * (rms(y) * (weight_offset + post_weight))     (post_norm or post_weight given)
+               = gate * y                                            (neither)
+        out    = residual_scale * residual + z
+        normed = rms(out) * (weight_offset + pre_weight)             (pre_norm or pre_weight given)
+
+    y [T, H] is the block's output, `out` the next residual stream, `normed` the
+    next block's input; rms(v) = v / sqrt(mean(v^2) + eps).  y, residual, out,
+    normed, gate and the weights are bf16 or fp32 (residual and out alike, both
+    weights alike); rows may be strided.  gate is a number or a tensor that
+    broadcasts to [T, H] ([H], [T, 1], ...); weights are [H], None for ones.
+    `out` and `normed` are allocated in the residual's type (y's without one)
+    unless given, and may be y or residual themselves.  want_out=False skips
+    `out`: a plain norm of y.
+
+    Returns out, (out, normed) with a norm after the block, or normed alone
+    with want_out=False."""
+    import torch
+    bgq = _api()
+    dev = _device(y, "y")
+    if y.dim() != 2:
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected [T, H]")
+    T, H = y.shape
+    n = MoeNorm()
+    n.y_type = _type(y, "y")
+    n.y_stride = _rows(y, "y", dev, T, H)
+    n.stream_type = n.y_type
+    with_normed = _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_scale, pre_norm,
+                             pre_weight, weight_offset, eps)
+    if not with_normed and normed is not None:
+        raise ValueError("normed is given without pre_norm or pre_weight")
+    if not want_out and (not with_normed or out is not None):
+        raise ValueError("want_out=False takes no out and needs pre_norm or pre_weight")
+    dtype = y.dtype if residual is None else residual.dtype
+    if out is not None and residual is None:
+        n.stream_type = _type(out, "out")
+    elif out is not None and out.dtype != dtype:
+        raise ValueError(f"out must have the residual's type {dtype}, got {out.dtype}")
+
+    def go(raw):
+        o, m = out, normed
+        if want_out:
+            if o is None:
+                o = torch.empty((T, H), dtype=dtype, device=dev)
+            n.out_stride = _rows(o, "out", dev, T, H)
+            n.out = o.data_ptr()
+        if with_normed:
+            if m is None:
+                m = torch.empty((T, H), dtype=dtype, device=dev)
+            n.normed_type = _type(m, "normed")
+            n.normed_stride = _rows(m, "normed", dev, T, H)
+            n.normed = m.data_ptr()
+        st = bgq.lib().moe_block_norm(ctypes.byref(n), y.data_ptr(), raw)
+        if st != 0:
+            raise bgq.MoeError(st, "moe_block_norm")
+        return (o, m) if want_out and with_normed else o if want_out else m
+
+    return _call(dev, stream, go)

@@ -331,6 +331,61 @@ moe_status moe_expert_ffn_forward_timed(const moe_problem* p, const void* x,
                                         void* out, void* ws, size_t ws_bytes,
                                         void* stream, void* const* events);
 
+/* Element types of the tensors below. */
+enum {
+    MOE_T_BF16 = 0,
+    MOE_T_FP32 = 1
+};
+
+/*
+ * Norms around a block, fused with the block's gate and the residual scale.
+ * With rms(v) = v / sqrt(mean(v^2) + eps) over a row's H values:
+ *
+ *   z      = gate_scale * gate * (rms(y) * (weight_offset + post_weight))   with MOE_N_POST
+ *            gate_scale * gate * y                                          without
+ *   out    = residual_scale * residual + z
+ *   normed = rms(out) * (weight_offset + pre_weight)                        if normed is given
+ *
+ * y is the block's output (for instance that of moe_expert_ffn_forward), out
+ * the next residual stream and normed the next block's input.  All arithmetic
+ * is fp32; out and normed are rounded once each, and normed is formed from the
+ * unrounded out.  Append-only: new fields go at the end.
+ */
+#define MOE_N_POST 1u           /* normalise y (post norm) */
+#define MOE_NORM_MAX_H 16384
+typedef struct {
+    int32_t T;                  /* rows, >= 0                                          */
+    int32_t H;                  /* values of a row, 1 <= H <= MOE_NORM_MAX_H           */
+    int32_t y_type;             /* MOE_T_* of y                                        */
+    int32_t stream_type;        /* of residual and out                                 */
+    int32_t normed_type;        /* of normed                                           */
+    int32_t weight_type;        /* of post_weight and pre_weight                       */
+    int32_t gate_type;          /* of gate                                             */
+    uint32_t flags;             /* MOE_N_*                                             */
+    float eps;                  /* >= 0                                                */
+    float residual_scale;
+    float gate_scale;
+    float weight_offset;        /* 0, or 1 for weights stored as their distance from 1 */
+    const void* residual;       /* [T, H]; NULL: no residual                           */
+    const void* post_weight;    /* [H]; NULL: weight 1 (post norm with MOE_N_POST)     */
+    const void* gate;           /* broadcast over [T, H] by its strides; NULL: 1       */
+    const void* pre_weight;     /* [H]; NULL: weight 1                                 */
+    void* out;                  /* [T, H]; NULL: not written (then normed is)          */
+    void* normed;               /* [T, H]; NULL: no norm after the block               */
+    int64_t y_stride;           /* elements from one row to the next, >= 0             */
+    int64_t residual_stride;    /* >= 0                                                */
+    int64_t out_stride;         /* >= H                                                */
+    int64_t normed_stride;      /* >= H                                                */
+    int64_t gate_stride_t;      /* >= 0; 0: the same gate for every token              */
+    int64_t gate_stride_h;      /* 1, or 0: one gate per token                         */
+} moe_norm;
+
+/* Rows are contiguous along H.  Pointers need the alignment of their element;
+ * rows that start on 16 bytes with H a multiple of 8 move as 16-byte loads.
+ * out and normed must not overlap each other or an input, except that either
+ * may be exactly y or residual (same address, type and row stride). */
+moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status s);
 
