@@ -93,7 +93,7 @@ def _call(dev, stream, f):
     """f(raw stream) with the device and stream current; no context in the usual case."""
     import torch
     if stream is None and dev.index == torch.cuda.current_device():
-        return f(torch.cuda.current_stream(dev).cuda_stream)
+        return f(torch._C._cuda_getCurrentRawStream(dev.index))  # current_stream() without its object
     with _ambient(dev, stream):
         return f(torch.cuda.current_stream(dev).cuda_stream)
 

@@ -123,7 +123,7 @@ def run_case(T, H, yt=BF, st=BF, wt=BF, gate="channel", post=True, pre=True, off
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,H", [
     (1, 2816), (1, 1), (3, 2), (5, 7), (2, 63), (7, 64), (9, 1001), (4, 2047), (33, 2048), (5, 2056), (8, 4096),
-    (3, 4104), (2, 8192), (2, 16384), (3, 16383), (5000, 64), (4099, 2040), (513, 704)])
+    (3, 4104), (2, 8192), (2, 16384), (3, 16383), (5000, 64), (4099, 2040), (513, 704), (1025, 504), (1024, 1024), (2, 8200)])
 def test_sizes(T, H):
     run_case(T, H)
 
