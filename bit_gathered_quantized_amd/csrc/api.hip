@@ -276,9 +276,55 @@ moe::NormArgs norm_args(const moe_norm* n, const void* y) {
     return a;
 }
 
+// A router's checks apart from its outputs.
+moe_status check_router(const moe_router* r) {
+    if (!r) return MOE_ERR_NULL;
+    if (!known_type(r->weight_type) || (r->flags & ~MOE_R_NORM)) return MOE_ERR_UNSUPPORTED;
+    if (r->T < 0 || r->H < 1 || r->E < 1 || r->k < 1 || r->k > r->E || r->H % 64) return MOE_ERR_SHAPE;
+    if (r->E > MOE_MAX_EXPERTS || r->k > moe::kRouterMaxK || r->H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
+    if (!(r->eps >= 0.f)) return MOE_ERR_SHAPE;
+    if (r->x_stride < r->H || r->x_stride > MOE_ROUTER_MAX_STRIDE) return MOE_ERR_SHAPE;
+    if (static_cast<int64_t>(r->T) * r->E > INT32_MAX) return MOE_ERR_SHAPE;
+    if (r->T == 0) return MOE_OK;
+    if (!r->weight) return MOE_ERR_NULL;
+    if (r->x_stride % 8 || !aligned(r->weight, 16) || !aligned(r->expert_scale, 4)) return MOE_ERR_ALIGN;
+    return MOE_OK;
+}
+
+hipError_t enqueue_router(const moe_router* r, const void* x, float* logits, int32_t* ids, float* weights,
+                          hipStream_t s) {
+    moe::RouterArgs a;
+    a.T = r->T;
+    a.H = r->H;
+    a.E = r->E;
+    a.weight_f32 = r->weight_type == MOE_T_FP32;
+    a.norm = r->flags & MOE_R_NORM;
+    a.eps = r->eps;
+    a.x_stride = r->x_stride;
+    a.x = static_cast<const uint16_t*>(x);
+    a.weight = r->weight;
+    a.logits = logits;
+    const hipError_t e = moe::launch_router_product(a, s);
+    if (e != hipSuccess) return e;
+    return moe::launch_router_topk(logits, r->T, r->E, r->k, r->expert_scale, ids, weights, s);
+}
+
 }  // namespace
 
 extern "C" {
+
+moe_status moe_router_forward(const moe_router* r, const void* x, float* logits, int32_t* topk_ids,
+                              float* topk_weights, void* stream) {
+    const moe_status st = check_router(r);
+    if (st != MOE_OK) return st;
+    if (r->T == 0) return MOE_OK;
+    if (!x || !logits || !topk_ids || !topk_weights) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
+        return MOE_ERR_ALIGN;
+    const hipError_t e =
+        enqueue_router(r, x, logits, topk_ids, topk_weights, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
 
 moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream) {
     const moe_status st = check_norm(n);
@@ -416,7 +462,7 @@ moe_status moe_router_topk(const float* logits, int32_t T, int32_t E, int32_t k,
     if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4))
         return MOE_ERR_ALIGN;
     if (static_cast<int64_t>(T) * E > INT32_MAX) return MOE_ERR_SHAPE;
-    const hipError_t e = moe::launch_router_topk(logits, T, E, k, topk_ids, topk_weights,
+    const hipError_t e = moe::launch_router_topk(logits, T, E, k, nullptr, topk_ids, topk_weights,
                                                   static_cast<hipStream_t>(stream));
     return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -280,9 +280,22 @@ hipError_t launch_gateup_wide(const FfnArgs& a, hipStream_t stream, const KTimin
 hipError_t launch_down_skinny(const FfnArgs& a, hipStream_t stream, const KTiming& t = {});
 hipError_t launch_down_wide(const FfnArgs& a, hipStream_t stream, const KTiming& t = {});
 hipError_t launch_combine(const FfnArgs& a, hipStream_t stream, const KTiming& t = {});
-hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* ids,
-                              float* weights, hipStream_t stream);
+// expert_scale: a factor of each expert's weight, or nullptr
+hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, const float* expert_scale,
+                              int32_t* ids, float* weights, hipStream_t stream);
 constexpr int kRouterMaxK = 64;
+
+// The router's product (router_product.hip).
+struct RouterArgs {
+    int32_t T, H, E;
+    bool weight_f32, norm;
+    float eps;
+    int64_t x_stride;
+    const uint16_t* x;   // [T, H] bf16
+    const void* weight;  // [E, H]
+    float* logits;       // [T, E]
+};
+hipError_t launch_router_product(const RouterArgs& a, hipStream_t stream);
 
 // The block norm (norm.hip).  Types as booleans (fp32, else bf16).
 struct NormArgs {

@@ -19,8 +19,8 @@ constexpr int kRouterPerLane = MOE_MAX_EXPERTS / 64;
 constexpr int kRouterTokensPerBlock = 4;
 
 __global__ __launch_bounds__(64 * kRouterTokensPerBlock) void moe_router_topk_kernel(
-    const float* __restrict__ logits, int32_t T, int32_t E, int32_t k, int32_t* __restrict__ ids,
-    float* __restrict__ weights) {
+    const float* __restrict__ logits, int32_t T, int32_t E, int32_t k,
+    const float* __restrict__ expert_scale, int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * kRouterTokensPerBlock + (threadIdx.x >> 6);
     if (t >= T) return;  // whole wave; no barrier follows
@@ -72,17 +72,18 @@ __global__ __launch_bounds__(64 * kRouterTokensPerBlock) void moe_router_topk_ke
     sum = __shfl(sum, 0);  // one rounding of the sum for every lane
     if (lane < k) {
         ids[static_cast<size_t>(t) * k + lane] = my_id;
-        weights[static_cast<size_t>(t) * k + lane] = ex / sum;
+        const float w = ex / sum;
+        weights[static_cast<size_t>(t) * k + lane] = expert_scale ? w * expert_scale[my_id] : w;
     }
 }
 
 }  // namespace
 
-hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, int32_t* ids,
-                              float* weights, hipStream_t stream) {
+hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, const float* expert_scale,
+                              int32_t* ids, float* weights, hipStream_t stream) {
     const dim3 grid((T + kRouterTokensPerBlock - 1) / kRouterTokensPerBlock);
     hipLaunchKernelGGL(moe_router_topk_kernel, grid, dim3(64 * kRouterTokensPerBlock), 0, stream,
-                       logits, T, E, k, ids, weights);
+                       logits, T, E, k, expert_scale, ids, weights);
     return hipGetLastError();
 }
 

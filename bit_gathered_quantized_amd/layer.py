@@ -1,4 +1,4 @@
-"""Binding of the operators around the expert FFN: the block norms.
+"""Binding of the operators around the expert FFN: the block norms and the router.
 
 As in the package itself, argument checks and marshalling only; the work runs
 in the HIP kernels of ``libmoeffn.so`` and PyTorch supplies memory and streams.
@@ -12,10 +12,11 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-__all__ = ["MoeNorm", "block_norm", "MOE_T_BF16", "MOE_T_FP32", "MOE_N_POST", "NORM_MAX_H"]
+__all__ = ["MoeNorm", "MoeRouter", "block_norm", "router_forward", "MOE_R_NORM", "MOE_T_BF16", "MOE_T_FP32", "MOE_N_POST", "NORM_MAX_H"]
 
 MOE_T_BF16, MOE_T_FP32 = 0, 1
 MOE_N_POST = 1
+MOE_R_NORM = 1
 NORM_MAX_H = 16384
 
 
@@ -28,6 +29,12 @@ class MoeNorm(ctypes.Structure):
                 ("residual", "post_weight", "gate", "pre_weight", "out", "normed")] + \
                [(n, ctypes.c_int64) for n in
                 ("y_stride", "residual_stride", "out_stride", "normed_stride", "gate_stride_t", "gate_stride_h")]
+
+
+class MoeRouter(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "E", "k", "weight_type")] + \
+               [("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("expert_scale", ctypes.c_void_p)]
 
 
 def _api():
@@ -194,5 +201,68 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None
         if st != 0:
             raise bgq.MoeError(st, "moe_block_norm")
         return (o, m) if want_out and with_normed else o if want_out else m
+
+    return _call(dev, stream, go)
+
+
+def _output(t, name, dev, shape, dtype):
+    """Data pointer of a given contiguous output."""
+    _on(t, name, dev)
+    if tuple(t.shape) != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def router_forward(x, weight, k, *, norm=True, eps=1e-6, expert_scale=None, logits=None, ids=None, weights=None,
+                   stream=None):
+    """The whole router: norm, product and top-k.
+
+        logits[t, e] = rstd_t * sum_c x[t, c] weight[e, c],   rstd_t = 1 / sqrt(mean(x_t^2) + eps)  (1 without norm)
+
+    x bf16 [T, H] (rows may be strided), weight [E, H] bf16 or fp32 with a norm's
+    weight or a router's scale already multiplied into its columns; H a multiple
+    of 64.  ids int32 [T, k] are the k largest logits in descending order (the
+    lower id first on ties), weights fp32 [T, k] their softmax, times
+    expert_scale[id] if given (fp32 [E]).  Products of x are exact and sums fp32
+    whichever type the weight has.  Returns (logits fp32 [T, E], ids, weights)."""
+    import torch
+    bgq = _api()
+    dev = _device(x, "x")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"x and weight must be [T, H] and [E, H], got {tuple(x.shape)} and {tuple(weight.shape)}")
+    T, H = x.shape
+    E = weight.shape[0]
+    if x.dtype is not torch.bfloat16:
+        raise ValueError(f"x must be bfloat16, got {x.dtype}")
+    r = MoeRouter()
+    r.T, r.H, r.E, r.k, r.eps, r.flags = T, H, E, k, eps, MOE_R_NORM if norm else 0
+    r.x_stride = _rows(x, "x", dev, T, H)
+    r.weight_type = _type(weight, "weight")
+    if not weight.is_contiguous():
+        raise ValueError("weight must be contiguous")
+    _rows(weight, "weight", dev, E, H)
+    r.weight = weight.data_ptr()
+    if expert_scale is not None:
+        if expert_scale.dtype is not torch.float32:
+            raise ValueError(f"expert_scale must be float32, got {expert_scale.dtype}")
+        r.expert_scale = _vector(expert_scale, "expert_scale", dev, E)
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be between 1 and the number of experts {E}, got {k}")
+
+    def go(raw):
+        lo, i, w = logits, ids, weights
+        if lo is None:
+            lo = torch.empty((T, E), dtype=torch.float32, device=dev)
+        if i is None:
+            i = torch.empty((T, k), dtype=torch.int32, device=dev)
+        if w is None:
+            w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        st = bgq.lib().moe_router_forward(ctypes.byref(r), x.data_ptr(),
+                                          _output(lo, "logits", dev, (T, E), torch.float32),
+                                          _output(i, "ids", dev, (T, k), torch.int32),
+                                          _output(w, "weights", dev, (T, k), torch.float32), raw)
+        if st != 0:
+            raise bgq.MoeError(st, "moe_router_forward")
+        return lo, i, w
 
     return _call(dev, stream, go)

@@ -386,6 +386,40 @@ typedef struct {
  * may be exactly y or residual (same address, type and row stride). */
 moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream);
 
+/*
+ * The whole router: norm, product and top-k.
+ *
+ *   logits[t, e] = rstd_t * sum_c x[t, c] weight[e, c]
+ *   rstd_t       = 1 / sqrt(mean_c x[t, c]^2 + eps) with MOE_R_NORM, else 1
+ *   ids, weights : moe_router_topk of the logits, each weight times
+ *                  expert_scale[id] if given
+ *
+ * A norm's weight or a router's scale is a factor of the columns of `weight`
+ * and is multiplied into it once, beforehand.  Products of x are exact and sums
+ * are fp32, for an fp32 weight too (finite values).
+ */
+#define MOE_R_NORM 1u
+typedef struct {
+    int32_t T;                 /* tokens, >= 0                                       */
+    int32_t H;                 /* multiple of 64, <= MOE_NORM_MAX_H                  */
+    int32_t E;                 /* experts, 1 <= E <= MOE_MAX_EXPERTS                 */
+    int32_t k;                 /* experts per token, 1 <= k <= min(E, 64)            */
+    int32_t weight_type;       /* MOE_T_* of weight                                  */
+    uint32_t flags;            /* MOE_R_*                                            */
+    float eps;                 /* >= 0                                               */
+    int64_t x_stride;          /* elements from one token of x to the next: a
+                                  multiple of 8, >= H, <= MOE_ROUTER_MAX_STRIDE      */
+    const void* weight;        /* [E, H], 16-byte aligned                            */
+    const float* expert_scale; /* [E] or NULL                                        */
+} moe_router;
+#define MOE_ROUTER_MAX_STRIDE (1 << 22)
+
+/* x bf16 [T, H], 16-byte aligned; logits fp32 [T, E]; topk_ids int32 [T, k];
+ * topk_weights fp32 [T, k].  Deterministic; a token's logits may differ in
+ * their last bits between batches of up to 16 tokens and larger ones. */
+moe_status moe_router_forward(const moe_router* r, const void* x, float* logits, int32_t* topk_ids,
+                              float* topk_weights, void* stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status s);
 
