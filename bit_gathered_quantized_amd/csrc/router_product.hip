@@ -5,15 +5,18 @@
 // it belongs in w once; then x enters the product as the bf16 it is, and rstd,
 // one number a row, multiplies the finished sum.  Products are exact, sums fp32.
 //
-// Few tokens (T <= 16): one workgroup an expert, its four waves cut the columns.
-// Bound by launch and load latency; the waves read w's row once and x from L2.
+// Few tokens (T <= 8): one workgroup an expert, its four waves cut the columns.
+// Bound by launch and load latency; the waves read w's row once and x from L2
+// (8 tokens, 128 experts, H 2816, fp32: 7.7 us with top-k).
 //
-// More tokens: 16 or 64 tokens by 32 experts a workgroup on
-// v_mfma_f32_16x16x32_bf16, eight waves cutting the columns and joined through
-// LDS in wave order.  An fp32 w goes in as three bf16 parts, hi + mid + lo = w to
-// the last bit (8 + 8 + 8 significant bits), three MFMAs instead of one; a row's
-// sum of squares is the diagonal of x x^T, one MFMA more, from operands already
-// in registers.
+// More tokens: 16, 32 or 64 tokens by as many experts a workgroup on
+// v_mfma_f32_16x16x32_bf16, its waves cutting the columns and joined through LDS
+// in wave order.  An fp32 w goes in as three bf16 parts, hi + mid + lo = w to the
+// last bit (8 + 8 + 8 significant bits), three MFMAs instead of one; a row's sum
+// of squares is the diagonal of x x^T, one MFMA more, from operands already in
+// registers.  Bound by cache reads: a tile reads its x and w rows once, so
+// larger tiles read less and smaller ones fill the GPU (rule below).  2048 tokens
+// and 128 experts: 14 us with bf16 weights, 17 us with fp32.
 #include "moe_internal.h"
 
 namespace moe {
@@ -132,74 +135,122 @@ __device__ __forceinline__ void split3(u32x4 a, u32x4 b, u32x4 (&p)[3]) {
     }
 }
 
-constexpr int kTileWaves = 8, kTileExperts = 32;
-
-template <int MT, bool kWF32>
-__global__ __launch_bounds__(64 * kTileWaves) void moe_router_product_tile(RouterArgs a) {
-    constexpr int kRows = 16 * MT, kW = kWF32 ? 4 : 2, kParts = kWF32 ? 3 : 1;
-    __shared__ float part[kTileWaves][kRows][kTileExperts];
-    __shared__ float sq[kTileWaves][kRows];
+// MT row blocks of 16 tokens, NT of 16 experts, WAVES cuts of the columns; each
+// wave keeps the operands of RING steps of 32 columns in flight.
+template <int MT, int NT, int WAVES, int RING, bool kWF32>
+__global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs a) {
+    constexpr int kRows = 16 * MT, kExperts = 16 * NT, kW = kWF32 ? 4 : 2, kRaw = kWF32 ? 2 : 1, kParts = kWF32 ? 3 : 1;
+    // wave-private turning buffers in the loop, then the waves' sums
+    union Smem {
+        u32x4 turn[WAVES][MT + NT * kRaw][64];
+        struct {
+            float part[WAVES][kRows][kExperts], sq[WAVES][kRows];
+        };
+    };
+    __shared__ Smem sm;
+    auto& part = sm.part;
+    auto& sq = sm.sq;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, q = lane >> 4;
     const int H = a.H, E = a.E;
-    const int t0 = blockIdx.x * kRows, e0 = blockIdx.y * kTileExperts;
-    const int rows = min(kRows, a.T - t0), experts = min(kTileExperts, E - e0);
+    const int t0 = blockIdx.x * kRows, e0 = blockIdx.y * kExperts;
+    const int rows = min(kRows, a.T - t0), experts = min(kExperts, E - e0);
     // rows past the batch and experts past E read zeros
     const uint32_t xrow = 2u * static_cast<uint32_t>(a.x_stride), wrow = static_cast<uint32_t>(H) * kW;
     const Rsrc rx = make_rsrc(a.x + t0 * a.x_stride, (rows - 1) * xrow + 2u * H);
     const Rsrc rw = make_rsrc(static_cast<const char*>(a.weight) + static_cast<size_t>(e0) * wrow, experts * wrow);
 
-    f32x4 acc[MT][2], gram[MT];
+    f32x4 acc[MT][NT], gram[MT];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = gram[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int steps = H / 32, s0 = steps * wave / kTileWaves, s1 = steps * (wave + 1) / kTileWaves;
-    uint32_t xat[MT];
+    for (int m = 0; m < MT; ++m) {
+        gram[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int m = 0; m < MT; ++m) xat[m] = (16 * m + lr) * xrow + 16u * q;
-    const uint32_t wat = lr * wrow + 8u * kW * q;
-#pragma unroll 2
-    for (int s = s0; s < s1; ++s) {
-        u32x4 x[MT], w[2][kParts];
-        u32x4 raw[2][kWF32 ? 2 : 1];
+        for (int n = 0; n < NT; ++n) acc[m][n] = gram[m];
+    }
+    const int steps = H / 32, s0 = steps * wave / WAVES, s1 = steps * (wave + 1) / WAVES;
+    // Loads are coalesced: 4 (fp32 weights: 8) lanes in a row read its 64 (128)
+    // bytes of a step.  The operand wants lane (lr, q) to hold columns 8 q .. 8 q + 7
+    // of row lr, so each 1 KB goes through LDS, 16-byte pieces XOR-swizzled so that
+    // neither side meets a bank twice.  Loading the operand layout directly costs a
+    // cache lookup a lane instead of one a row.
+    const int r4 = lane >> 2, p4 = lane & 3, r8 = lane >> 3, p8 = lane & 7;
+    const uint32_t xat = r4 * xrow + 16u * p4;
+    const uint32_t wat = kWF32 ? r8 * wrow + 16u * p8 : r4 * wrow + 16u * p4;
+    const int put4 = 4 * r4 + (p4 ^ (r4 >> 2 & 3)), get4 = 4 * lr + (q ^ (lr >> 2 & 3));
+    u32x4 x[RING][MT], raw[RING][NT][kRaw];
+    auto load = [&](int slot, int s) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < (kWF32 ? 2 : 1); ++h)
-                raw[n][h] = load16(rw, wat + 16u * n * wrow + 32u * kW * s + 16u * h);
+            for (int h = 0; h < kRaw; ++h)
+                raw[slot][n][h] = load16(rw, wat + (16u * n + 8u * h) * wrow + 32u * kW * s);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) x[m] = load16(rx, xat[m] + 64u * s);
+        for (int m = 0; m < MT; ++m) x[slot][m] = load16(rx, xat + 16u * m * xrow + 64u * s);
+    };
+    auto compute = [&](int slot) {
+        u32x4 (&buf)[MT + NT * kRaw][64] = sm.turn[wave];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            if constexpr (kWF32)
-                split3(raw[n][0], raw[n][1], w[n]);
-            else
-                w[n][0] = raw[n][0];
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (kWF32) {  // rows of 8 pieces over two buffers, row r8 + 8 h
+#pragma unroll
+                for (int h = 0; h < 2; ++h) buf[MT + 2 * n + h][8 * r8 + (p8 ^ ((r8 + 8 * h) >> 1 & 7))] = raw[slot][n][h];
+            } else {
+                buf[MT + n][put4] = raw[slot][n][0];
+            }
         }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) buf[m][put4] = x[slot][m];
+        __builtin_amdgcn_wave_barrier();
+        u32x4 w[NT][kParts], xo[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xo[m] = buf[m][get4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (kWF32) {
+                const u32x4* row = &buf[MT + 2 * n + (lr >> 3)][8 * (lr & 7)];
+                split3(row[(2 * q) ^ (lr >> 1 & 7)], row[(2 * q + 1) ^ (lr >> 1 & 7)], w[n]);
+            } else {
+                w[n][0] = buf[MT + n][get4];
+            }
+        }
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int p = 0; p < kParts; ++p)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) acc[m][n] = mfma16(x[m], w[n][p], acc[m][n]);
+                for (int n = 0; n < NT; ++n) acc[m][n] = mfma16(xo[m], w[n][p], acc[m][n]);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) gram[m] = mfma16(x[m], x[m], gram[m]);
+        for (int m = 0; m < MT; ++m) gram[m] = mfma16(xo[m], xo[m], gram[m]);
+    };
+#pragma unroll
+    for (int i = 0; i < RING; ++i) load(i, min(s0 + i, steps - 1));
+    for (int s = s0; s < s1; s += RING) {
+#pragma unroll
+        for (int i = 0; i < RING; ++i) {
+            if (s + i < s1) compute(i);
+            // past the wave's share the last step is read again, for nothing
+            load(i, min(s + i + RING, steps - 1));
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
+    __syncthreads();  // the turning buffers become the sums
     // lane (lr, q) holds rows 4 q + v and column lr of each 16 x 16 product
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int r = 16 * m + 4 * q + v;
-            part[wave][r][lr] = acc[m][0][v];
-            part[wave][r][16 + lr] = acc[m][1][v];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) part[wave][r][16 * n + lr] = acc[m][n][v];
             if (lr == 4 * q + v) sq[wave][r] = gram[m][v];
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * kTileExperts; i += 64 * kTileWaves) {
-        const int r = i / kTileExperts, e = i % kTileExperts;
+    for (int i = threadIdx.x; i < kRows * kExperts; i += 64 * WAVES) {
+        const int r = i / kExperts, e = i % kExperts;
         float v = 0.f, s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kTileWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             v += part[w][r][e];
             s += sq[w][r];
         }
@@ -215,32 +266,40 @@ void few(const RouterArgs& a, hipStream_t s) {
     else
         hipLaunchKernelGGL((moe_router_product_few<TM, false>), dim3(a.E), dim3(256), 0, s, a);
 }
-template <int MT>
+template <int MT, int NT, int WAVES, int RING>
 void tile(const RouterArgs& a, hipStream_t s) {
-    const dim3 grid((a.T + 16 * MT - 1) / (16 * MT), (a.E + kTileExperts - 1) / kTileExperts);
+    const dim3 grid((a.T + 16 * MT - 1) / (16 * MT), (a.E + 16 * NT - 1) / (16 * NT)), block(64 * WAVES);
     if (a.weight_f32)
-        hipLaunchKernelGGL((moe_router_product_tile<MT, true>), grid, dim3(64 * kTileWaves), 0, s, a);
+        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, RING, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((moe_router_product_tile<MT, false>), grid, dim3(64 * kTileWaves), 0, s, a);
+        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, RING, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
 hipError_t launch_router_product(const RouterArgs& a, hipStream_t s) {
-    if (a.T <= 1)
+    const int64_t T = a.T, E = a.E;
+    // workgroups of the tile of m row blocks by n blocks of experts
+    auto groups = [&](int m, int n) { return (T + 16 * m - 1) / (16 * m) * ((E + 16 * n - 1) / (16 * n)); };
+    if (T <= 1)
         few<1>(a, s);
-    else if (a.T <= 2)
+    else if (T <= 2)
         few<2>(a, s);
-    else if (a.T <= 4)
+    else if (T <= 4)
         few<4>(a, s);
-    else if (a.T <= 8)
+    else if (T <= 8)
         few<8>(a, s);
-    else if (a.T <= 16)
-        few<16>(a, s);
-    else if (static_cast<int64_t>(a.T) * a.E < 64 * 128 * 32)
-        tile<1>(a, s);
+    // the largest tile that still gives every CU (32 x 32: every other) a workgroup.
+    // Measured with top-k,
+    // 64 x 64 | 32 x 32 | 16 x 16: 8192 tokens and 128 experts 29 | 46 | 105 us,
+    // 2048 and 128 22 | 14 | 26 us, 512 and 128 18 | 11.3 | 11.2 us (fp32 weights
+    // 28 | 16 | 13 us), 64 and 128 (fp32) 24 | 15 | 10 us
+    else if (groups(4, 4) >= 256)
+        tile<4, 4, 8, 1>(a, s);
+    else if (groups(2, 2) >= 128)
+        tile<2, 2, 8, 2>(a, s);
     else
-        tile<4>(a, s);
+        tile<1, 1, 16, 4>(a, s);
     return hipGetLastError();
 }
 

@@ -416,7 +416,7 @@ typedef struct {
 
 /* x bf16 [T, H], 16-byte aligned; logits fp32 [T, E]; topk_ids int32 [T, k];
  * topk_weights fp32 [T, k].  Deterministic; a token's logits may differ in
- * their last bits between batches of up to 16 tokens and larger ones. */
+ * their last bits with the number of tokens in the batch. */
 moe_status moe_router_forward(const moe_router* r, const void* x, float* logits, int32_t* topk_ids,
                               float* topk_weights, void* stream);
 

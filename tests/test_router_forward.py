@@ -66,7 +66,7 @@ def check(x, w, k, scale, got, norm=True, eps=1e-6):
     rstd = torch.rsqrt(xd.square().mean(-1, keepdim=True) + eps) if norm else torch.ones(T, 1, device="cuda").double()
     ref = rstd * (xd @ wd.T)
     size = rstd * (xd.abs() @ wd.abs().T)
-    if T <= 16:
+    if T <= 8:
         L = 8 * math.ceil(H / 2048) + 10
     else:
         L = 32 * math.ceil(H / 256) * (3 if w.dtype is torch.float32 else 1) + 8
