@@ -11,13 +11,13 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
-from .layer import MoeNorm, MoeRouter, block_norm, router_forward
+from .layer import MoeLayer, MoeLayerDesc, MoeNorm, MoeRouter, block_norm, router_forward
 
 __all__ = [
     "MoeError", "lib", "LIB_PATH", "MOE_F_FP32_OUT", "MOE_F_FP32_INTERMEDIATE", "MOE_F_SWIGLU",
     "max_tiles", "workspace_bytes", "workspace_layout", "sort_build_tiles",
     "expert_ffn_forward", "router_topk", "status_string", "EXPORTED_SYMBOLS",
-    "block_norm", "router_forward",
+    "block_norm", "router_forward", "MoeLayer",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoeffn.so")
@@ -37,7 +37,7 @@ EXPORTED_SYMBOLS = (
     "moe_ffn_workspace_layout", "moe_expert_ffn_forward",
     "moe_expert_ffn_forward_timed", "moe_expert_ffn_forward_presorted", "moe_router_topk",
     "moe_status_string", "moe_expert_ffn_forward_noalloc", "moe_block_norm",
-    "moe_router_forward",
+    "moe_router_forward", "moe_layer_workspace_bytes", "moe_layer_forward",
 )
 MOE_ERR_SCRATCH = -7
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -101,6 +101,11 @@ def lib():
         L.moe_block_norm.restype = i32
         L.moe_router_forward.argtypes = [ctypes.POINTER(MoeRouter), P, P, P, P, P]
         L.moe_router_forward.restype = i32
+        L.moe_layer_workspace_bytes.argtypes = [ctypes.POINTER(MoeProblem)]
+        L.moe_layer_workspace_bytes.restype = sz
+        L.moe_layer_forward.argtypes = [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeLayerDesc), P,
+                                        ctypes.POINTER(MoeNorm), P, sz, P]
+        L.moe_layer_forward.restype = i32
         _lib = L
     return _lib
 

@@ -113,11 +113,12 @@ moe_status forward_impl(const moe_problem* p, const void* x, const int32_t* ids,
                         const float* topk_w, const uint32_t* w_gu, const void* s_gu,
                         const void* b_gu, const uint32_t* w_d, const void* s_d,
                         const void* b_d, void* out, void* ws, size_t ws_bytes, void* stream,
-                        void* const* events, const int32_t* presorted, bool want_presorted) {
+                        void* const* events, const int32_t* presorted, bool want_presorted,
+                        bool combine = true) {
     const moe_status st = check_problem(p);
     if (st != MOE_OK) return st;
     if (p->T == 0) return MOE_OK;
-    if (!x || !ids || !topk_w || !w_gu || !s_gu || !b_gu || !w_d || !s_d || !b_d || !out)
+    if (!x || !ids || !topk_w || !w_gu || !s_gu || !b_gu || !w_d || !s_d || !b_d || (combine && !out))
         return MOE_ERR_NULL;
     if (want_presorted && !presorted) return MOE_ERR_NULL;
     if (presorted && !aligned(presorted, 4)) return MOE_ERR_ALIGN;
@@ -217,7 +218,7 @@ moe_status forward_impl(const moe_problem* p, const void* x, const int32_t* ids,
     if (moe::launch_gateup_wide(f, s, kt(2)) != hipSuccess) return MOE_ERR_HIP;
     if (moe::launch_down_skinny(f, s, kt(3)) != hipSuccess) return MOE_ERR_HIP;
     if (moe::launch_down_wide(f, s, kt(4)) != hipSuccess) return MOE_ERR_HIP;
-    if (moe::launch_combine(f, s, kt(5)) != hipSuccess) return MOE_ERR_HIP;
+    if (combine && moe::launch_combine(f, s, kt(5)) != hipSuccess) return MOE_ERR_HIP;
     return MOE_OK;
 }
 
@@ -291,8 +292,7 @@ moe_status check_router(const moe_router* r) {
     return MOE_OK;
 }
 
-hipError_t enqueue_router(const moe_router* r, const void* x, float* logits, int32_t* ids, float* weights,
-                          hipStream_t s) {
+moe::RouterArgs router_args(const moe_router* r, const void* x, float* logits) {
     moe::RouterArgs a;
     a.T = r->T;
     a.H = r->H;
@@ -304,14 +304,185 @@ hipError_t enqueue_router(const moe_router* r, const void* x, float* logits, int
     a.x = static_cast<const uint16_t*>(x);
     a.weight = r->weight;
     a.logits = logits;
-    const hipError_t e = moe::launch_router_product(a, s);
+    return a;
+}
+
+hipError_t enqueue_router(const moe_router* r, const void* x, float* logits, int32_t* ids, float* weights,
+                          hipStream_t s) {
+    const hipError_t e = moe::launch_router_product(router_args(r, x, logits), s);
     if (e != hipSuccess) return e;
     return moe::launch_router_topk(logits, r->T, r->E, r->k, r->expert_scale, ids, weights, s);
+}
+
+static_assert(moe::kLayerFewTokens == MOE_LAYER_FEW_TOKENS, "few-token limit");
+
+// Byte offsets in the layer's workspace.
+struct LayerLayout {
+    size_t counters, logits, ids, weights, n, nsum, h, hsum, y, ffn, total;
+    int32_t num_counters;
+    bool few;
+};
+LayerLayout layer_layout(const moe_problem* p) {
+    LayerLayout l = {};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes);
+        return at;
+    };
+    const size_t T = p->T, A = T * p->k, H = p->H, I = p->I;
+    l.few = p->T <= MOE_LAYER_FEW_TOKENS;
+    l.logits = take(4 * T * p->E);
+    if (l.few) {
+        l.num_counters = static_cast<int32_t>(2 * moe::kLayerRanges + moe::kLayerFewTokens + 2 * A + 1);
+        l.counters = take(4 * static_cast<size_t>(l.num_counters));
+        l.n = take(4 * T * H);
+        l.nsum = take(8 * T * (H / 32));
+        l.h = take(4 * A * I);
+        l.hsum = take(8 * A * (I / 16));
+        l.y = take(4 * A * H);
+    } else {
+        l.ids = take(4 * A);
+        l.weights = take(4 * A);
+        l.n = take(2 * T * H);
+        l.ffn = take(make_layout(p).total);
+    }
+    l.total = off;
+    return l;
+}
+
+moe_status check_layer_problem(const moe_problem* p) {
+    const moe_status st = check_problem(p);
+    if (st != MOE_OK) return st;
+    if ((p->flags & MOE_F_FP32_OUT) || p->k > moe::kRouterMaxK) return MOE_ERR_UNSUPPORTED;
+    return static_cast<int64_t>(p->T) * p->E > INT32_MAX ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+bool rows16(const void* q, int64_t stride, int32_t type) {
+    return !q || (aligned(q, 16) && stride * static_cast<int64_t>(type_size(type)) % 16 == 0);
 }
 
 }  // namespace
 
 extern "C" {
+
+size_t moe_layer_workspace_bytes(const moe_problem* p) {
+    return check_layer_problem(p) == MOE_OK ? layer_layout(p).total : 0;
+}
+
+moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const void* x, const moe_norm* tail, void* ws,
+                             size_t ws_bytes, void* stream) {
+    moe_status st = check_layer_problem(p);
+    if (st != MOE_OK) return st;
+    if (!l || !tail) return MOE_ERR_NULL;
+    if (!known_type(l->norm_type) || (l->flags & ~MOE_L_NORM)) return MOE_ERR_UNSUPPORTED;
+    moe_router r;
+    r.T = p->T;
+    r.H = p->H;
+    r.E = p->E;
+    r.k = p->k;
+    r.weight_type = l->router_type;
+    r.flags = l->router_flags;
+    r.eps = l->eps;
+    r.x_stride = p->H;
+    r.weight = l->router_weight;
+    r.expert_scale = l->expert_scale;
+    if ((st = check_router(&r)) != MOE_OK) return st;
+    moe_norm t = *tail;
+    t.y_type = MOE_T_FP32;
+    t.y_stride = p->H;
+    if (t.T != p->T || t.H != p->H) return MOE_ERR_SHAPE;
+    if ((st = check_norm(&t)) != MOE_OK) return st;
+    if (p->T == 0) return MOE_OK;
+    if (!x || !l->w_gateup || !l->s_gateup || !l->b_gateup || !l->w_down || !l->s_down || !l->b_down) return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(l->norm_weight, 16) || !aligned(l->w_gateup, 16) || !aligned(l->s_gateup, 16) ||
+        !aligned(l->b_gateup, 16) || !aligned(l->w_down, 16) || !aligned(l->s_down, 16) || !aligned(l->b_down, 16) ||
+        !aligned(l->topk_ids, 4) || !aligned(l->topk_weights, 4) || !aligned(ws, kAlign) ||
+        !rows16(t.residual, t.residual_stride, t.stream_type) || !rows16(t.out, t.out_stride, t.stream_type) ||
+        !rows16(t.normed, t.normed_stride, t.normed_type) || !rows16(t.post_weight, 0, 0) ||
+        !rows16(t.pre_weight, 0, 0) || (t.gate && t.gate_stride_h && !rows16(t.gate, t.gate_stride_t, t.gate_type)))
+        return MOE_ERR_ALIGN;
+    const LayerLayout y = layer_layout(p);
+    if (!ws || ws_bytes < y.total) return MOE_ERR_WORKSPACE;
+
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char* base = static_cast<char*>(ws);
+    float* const logits = reinterpret_cast<float*>(base + y.logits);
+    if (y.few) {
+        moe::LayerArgs a = {};
+        a.T = p->T;
+        a.k = p->k;
+        a.E = p->E;
+        a.H = p->H;
+        a.I = p->I;
+        a.gs = p->group_size;
+        a.bits = p->bits;
+        a.swiglu = p->flags & MOE_F_SWIGLU;
+        a.norm = l->flags & MOE_L_NORM;
+        a.norm_f32 = l->norm_type == MOE_T_FP32;
+        a.eps = l->eps;
+        a.weight_offset = l->weight_offset;
+        a.router = router_args(&r, x, logits);
+        a.expert_scale = l->expert_scale;
+        a.x = static_cast<const uint16_t*>(x);
+        a.norm_weight = a.norm ? l->norm_weight : nullptr;
+        a.w_gu = l->w_gateup;
+        a.w_d = l->w_down;
+        a.s_gu = static_cast<const uint16_t*>(l->s_gateup);
+        a.b_gu = static_cast<const uint16_t*>(l->b_gateup);
+        a.s_d = static_cast<const uint16_t*>(l->s_down);
+        a.b_d = static_cast<const uint16_t*>(l->b_down);
+        a.out_ids = l->topk_ids;
+        a.out_weights = l->topk_weights;
+        a.tail = norm_args(&t, nullptr);
+        const int A = p->T * p->k;
+        a.counters = reinterpret_cast<int32_t*>(base + y.counters);
+        a.num_counters = y.num_counters;
+        a.claim_gateup = a.counters;
+        a.claim_down = a.claim_gateup + moe::kLayerRanges;
+        a.claim_token = a.claim_down + moe::kLayerRanges;
+        a.done_gateup = a.claim_token + moe::kLayerFewTokens;
+        a.done_down = a.done_gateup + A;
+        a.failed = a.done_down + A;
+        a.logits = logits;
+        a.n = reinterpret_cast<uint16_t*>(base + y.n);
+        a.nsum = reinterpret_cast<float*>(base + y.nsum);
+        a.h = reinterpret_cast<uint16_t*>(base + y.h);
+        a.hsum = reinterpret_cast<float*>(base + y.hsum);
+        a.y = reinterpret_cast<float*>(base + y.y);
+        return moe::launch_layer_few(a, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+    }
+
+    const void* n = x;
+    if (l->flags & MOE_L_NORM) {
+        moe::NormArgs a = {};
+        a.T = p->T;
+        a.H = p->H;
+        a.weight_f32 = l->norm_type == MOE_T_FP32;
+        a.eps = l->eps;
+        a.gate_scale = 1.f;
+        a.weight_offset = l->weight_offset;
+        a.y = x;
+        a.y_stride = p->H;
+        a.pre_weight = l->norm_weight;
+        a.normed = base + y.n;
+        a.normed_stride = p->H;
+        if (moe::launch_block_norm(a, s) != hipSuccess) return MOE_ERR_HIP;
+        n = base + y.n;
+    }
+    int32_t* const ids = l->topk_ids ? l->topk_ids : reinterpret_cast<int32_t*>(base + y.ids);
+    float* const weights = l->topk_weights ? l->topk_weights : reinterpret_cast<float*>(base + y.weights);
+    if (enqueue_router(&r, x, logits, ids, weights, s) != hipSuccess) return MOE_ERR_HIP;
+    const moe_ws_layout f = make_layout(p);
+    st = forward_impl(p, n, ids, weights, l->w_gateup, l->s_gateup, l->b_gateup, l->w_down, l->s_down, l->b_down, nullptr,
+                      base + y.ffn, f.total, stream, nullptr, nullptr, false, false);
+    if (st != MOE_OK) return st;
+    moe::NormArgs a = norm_args(&t, base + y.ffn + f.y);
+    a.ids = ids;
+    a.k = p->k;
+    a.E = p->E;
+    return moe::launch_block_norm(a, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
 
 moe_status moe_router_forward(const moe_router* r, const void* x, float* logits, int32_t* topk_ids,
                               float* topk_weights, void* stream) {

@@ -1775,15 +1775,15 @@ __global__ __launch_bounds__(kThreads, (kWideWgsPerCu<DownWideSmem<kF32H, MAXG, 
 // (a sum of floors never exceeds the floor of the sum).  The height of a wide
 // tile is no bound: with bm_big = 32 an expert of 33 rows gives tiles of 17
 // and 16 rows.
-static int skinny_grid(const FfnArgs& a) {
+static inline int skinny_grid(const FfnArgs& a) {
     const int A = a.T * a.k;
     return min(a.max_skinny, min(a.E, A) + (a.skinny_only ? A / kBmSmall : 0));
 }
-static int wide_grid(const FfnArgs& a) { return a.skinny_only ? 0 : a.max_tiles; }
+static inline int wide_grid(const FfnArgs& a) { return a.skinny_only ? 0 : a.max_tiles; }
 
 // No tile can be wide: nothing to launch, but the timing events still mark
 // the (empty) interval.
-static hipError_t skip_launch(hipStream_t stream, const KTiming& t) {
+static inline hipError_t skip_launch(hipStream_t stream, const KTiming& t) {
     if (t.start != nullptr && t.stop != nullptr) {
         hipError_t e = hipEventRecord(t.start, stream);
         if (e == hipSuccess) e = hipEventRecord(t.stop, stream);

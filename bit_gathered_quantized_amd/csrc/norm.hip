@@ -18,7 +18,7 @@
 //
 // Every load of a row is issued before the first use: y, residual, weights and
 // gate are independent, so a row pays one memory latency.
-#include "moe_internal.h"
+#include "block_norm.h"
 
 namespace moe {
 namespace {
@@ -27,138 +27,27 @@ namespace {
 template <int WAVES>
 constexpr int kNormThreads = WAVES == 1 ? 256 : 64 * WAVES;
 
-// A buffer resource over one row of a tensor (p the same in every lane of a
-// wave).  Loads past its end, or from a tensor that is absent (p == nullptr),
-// read nothing and return zeros, stores there are dropped: no branch stands
-// between the loads of a row, so they are all in flight together.
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-__device__ __forceinline__ Rsrc row_rsrc(const void* p, int64_t row_bytes, int64_t row, int H, int size) {
-    const char* q = static_cast<const char*>(p) + (p ? row * row_bytes : 0);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(q), 0, p ? H * size : 0, 0x00020000);
-}
-
-// VEC values as loaded: fp32 in lo and hi, bf16 in lo alone.
-template <int VEC>
-struct Raw {
-    u32x4 lo, hi;
-};
-template <>
-struct Raw<1> {
-    uint32_t u;
-};
-// `h` is `r` for an fp32 tensor and an empty resource for a bf16 one.
-template <int VEC>
-__device__ __forceinline__ Raw<VEC> load_raw(Rsrc r, Rsrc h, int c, bool f32) {
-    Raw<VEC> v;
-    if constexpr (VEC == 1) {
-        const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(h, 4 * c, 0, 0);
-        v.u = f32 ? w : static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * c, 0, 0)) << 16;
-    } else {
-        const int at = f32 ? 4 * c : 2 * c;
-        v.lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
-        v.hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(h, at + 16, 0, 0));
-    }
-    return v;
-}
-// The same for a type known when compiling.
-template <int VEC, bool kF32>
-__device__ __forceinline__ Raw<VEC> load_raw(Rsrc r, int c) {
-    Raw<VEC> v;
-    if constexpr (VEC == 1) {
-        if constexpr (kF32)
-            v.u = __builtin_amdgcn_raw_buffer_load_b32(r, 4 * c, 0, 0);
-        else
-            v.u = static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(r, 2 * c, 0, 0)) << 16;
-    } else {
-        v.lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (kF32 ? 4 : 2) * c, 0, 0));
-        if constexpr (kF32)
-            v.hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 4 * c + 16, 0, 0));
-    }
-    return v;
-}
-template <int VEC>
-__device__ __forceinline__ float value(const Raw<VEC>& r, int i, bool f32) {
-    if constexpr (VEC == 1) {
-        return __uint_as_float(r.u);
-    } else {
-        const uint32_t w = i < 4 ? r.lo[i & 3] : r.hi[i & 3], p = r.lo[i >> 1];
-        return __uint_as_float(f32 ? w : (i & 1 ? p & 0xFFFF0000u : p << 16));
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void store_values(Rsrc r, int c, const float (&v)[VEC], bool f32) {
-    if constexpr (VEC == 1) {
-        if (f32)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, 4 * c, 0, 0);
-        else
-            __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v[0]), r, 2 * c, 0, 0);
-    } else if (f32) {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), r, 4 * c, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]}), r, 4 * c + 16, 0,
-                                               0);
-    } else {
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                     pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])},
-                                               r, 2 * c, 0, 0);
-    }
-}
-
-// Sum of v over the WAVES waves that share a row, the same value in every
-// thread: lanes by exchange, waves through LDS in wave order.
-template <int WAVES>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
-    if constexpr (WAVES > 1) {
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) v += lds[w];
-    }
-    return v;
-}
-
 // kYF32, kSF32: y, and residual and out, are fp32.  kSlots: y is the fp32
 // [T * k, H] output of the down matmul, already weighted; row t is the sum of
 // its k slots in slot order (slots whose expert id is out of range were never
 // written and are skipped).
 template <int WAVES, int NV, int VEC, bool kYF32, bool kSF32, bool kSlots>
 __global__ __launch_bounds__(kNormThreads<WAVES>) void moe_block_norm_kernel(NormArgs a) {
+    using namespace norm;
     constexpr int kRows = kNormThreads<WAVES> / 64 / WAVES, kStep = 64 * WAVES * VEC;
     __shared__ float lds[2][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + (WAVES == 1 ? wave : 0);
     if (t >= a.T) return;  // whole waves of one row: no barrier is left waiting
     const int c0 = VEC * (WAVES == 1 ? threadIdx.x & 63 : threadIdx.x);
-    const int H = a.H;
-    const bool wf32 = a.weight_f32, gf32 = a.gate_f32, channel = a.gate != nullptr && a.gate_stride_h != 0;
-    constexpr int kYSize = kYF32 ? 4 : 2, kSSize = kSF32 ? 4 : 2;
-    const int wsize = wf32 ? 4 : 2, gsize = gf32 ? 4 : 2;
-    const Rsrc none = row_rsrc(nullptr, 0, 0, 0, 0);
-    const Rsrc sy = row_rsrc(kSlots ? nullptr : a.y, a.y_stride * kYSize, t, H, kYSize);
-    const Rsrc sr = row_rsrc(a.residual, a.residual_stride * kSSize, t, H, kSSize);
-    const Rsrc sp = row_rsrc(a.post_weight, 0, 0, H, wsize), sn = row_rsrc(a.pre_weight, 0, 0, H, wsize);
-    const Rsrc sg = row_rsrc(channel ? a.gate : nullptr, a.gate_stride_t * gsize, t, H, gsize);
-    const Rsrc hp = wf32 ? sp : none, hn = wf32 ? sn : none, hg = gf32 ? sg : none;
-
-    // 16 values a thread in 16-wave workgroups: 128 registers, so the gate and
-    // the last weights are loaded once the others are done with
-    constexpr bool kLate = VEC == 1 && NV >= 16;
-    Raw<VEC> ry[NV], rr[NV], rp[NV], rn[NV], rg[NV];
+    Raw<VEC> ry[NV];
+    if constexpr (!kSlots) {
+        const Rsrc sy = row_rsrc(a.y, a.y_stride * (kYF32 ? 4 : 2), t, a.H, kYF32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = c0 + i * kStep;
-        if constexpr (!kSlots) ry[i] = load_raw<VEC, kYF32>(sy, c);
-        rr[i] = load_raw<VEC, kSF32>(sr, c);
-        rp[i] = load_raw<VEC>(sp, hp, c, wf32);
-        if constexpr (!kLate) rg[i] = load_raw<VEC>(sg, hg, c, gf32);
-        if constexpr (!kLate) rn[i] = load_raw<VEC>(sn, hn, c, wf32);
+        for (int i = 0; i < NV; ++i) ry[i] = load_raw<VEC, kYF32>(sy, c0 + i * kStep);
     }
-    float g0 = a.gate_scale;
-    if (a.gate && !channel)
-        g0 *= gf32 ? static_cast<const float*>(a.gate)[t * a.gate_stride_t]
-                   : bf16_to_f32(static_cast<const uint16_t*>(a.gate)[t * a.gate_stride_t]);
+    Row<WAVES, NV, VEC, kSF32> row;
+    row.load(a, t, c0);
     float z[NV][VEC];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -173,7 +62,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void moe_block_norm_kernel(Nor
                 const int64_t s = t * a.k + min(j0 + u, a.k - 1);
                 const int32_t id = a.ids[s];
                 const bool ok = j0 + u < a.k && id >= 0 && id < a.E;
-                const Rsrc rs = row_rsrc(ok ? a.y : nullptr, 4 * static_cast<int64_t>(H), s, H, 4);
+                const Rsrc rs = row_rsrc(ok ? a.y : nullptr, 4 * static_cast<int64_t>(a.H), s, a.H, 4);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) r[u][i] = load_raw<VEC, true>(rs, c0 + i * kStep);
             }
@@ -185,55 +74,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void moe_block_norm_kernel(Nor
                     for (int v = 0; v < VEC; ++v) z[i][v] += value(r[u][i], v, true);
         }
     }
-
-    if (a.post) {
-        float ss = 0.f;  // values past H are zeros
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) ss = fmaf(z[i][v], z[i][v], ss);
-        const float rstd = 1.f / sqrtf(row_sum<WAVES>(ss, lds[0]) / H + a.eps);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                z[i][v] *= rstd * (a.post_weight ? a.weight_offset + value(rp[i], v, wf32) : 1.f);
-    }
-    if constexpr (kLate) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) rg[i] = load_raw<VEC>(sg, hg, c0 + i * kStep, gf32);
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = c0 + i * kStep < H;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            z[i][v] *= channel ? g0 * value(rg[i], v, gf32) : g0;
-            if (a.residual) z[i][v] = fmaf(a.residual_scale, value(rr[i], v, kSF32), z[i][v]);
-            // past H the zeros may have met an infinite factor: left out
-            ss = in ? fmaf(z[i][v], z[i][v], ss) : ss;
-        }
-    }
-    if constexpr (kLate) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) rn[i] = load_raw<VEC>(sn, hn, c0 + i * kStep, wf32);
-    }
-    const Rsrc so = row_rsrc(a.out, a.out_stride * kSSize, t, H, kSSize);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) store_values(so, c0 + i * kStep, z[i], kSF32);
-    if (a.normed) {
-        const int nsize = a.normed_f32 ? 4 : 2;
-        const Rsrc sm = row_rsrc(a.normed, a.normed_stride * nsize, t, H, nsize);
-        const float rstd = 1.f / sqrtf(row_sum<WAVES>(ss, lds[1]) / H + a.eps);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v)
-                z[i][v] *= rstd * (a.pre_weight ? a.weight_offset + value(rn[i], v, wf32) : 1.f);
-            store_values(sm, c0 + i * kStep, z[i], a.normed_f32);
-        }
-    }
+    row.finish(a, t, c0, z, lds);
 }
 
 template <int WAVES, int NV, int VEC, bool kYF32, bool kSF32, bool kSlots = false>

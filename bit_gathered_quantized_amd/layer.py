@@ -1,4 +1,5 @@
-"""Binding of the operators around the expert FFN: the block norms and the router.
+"""Binding of the operators around the expert FFN: the block norms, the router
+and the whole layer.
 
 As in the package itself, argument checks and marshalling only; the work runs
 in the HIP kernels of ``libmoeffn.so`` and PyTorch supplies memory and streams.
@@ -12,7 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-__all__ = ["MoeNorm", "MoeRouter", "block_norm", "router_forward", "MOE_R_NORM", "MOE_T_BF16", "MOE_T_FP32", "MOE_N_POST", "NORM_MAX_H"]
+__all__ = ["MoeNorm", "MoeRouter", "MoeLayerDesc", "MoeLayer", "block_norm", "router_forward", "MOE_R_NORM", "MOE_T_BF16", "MOE_T_FP32", "MOE_N_POST", "NORM_MAX_H"]
 
 MOE_T_BF16, MOE_T_FP32 = 0, 1
 MOE_N_POST = 1
@@ -105,6 +106,25 @@ def _call(dev, stream, f):
         return f(torch.cuda.current_stream(dev).cuda_stream)
 
 
+def _gate(n, gate, dev, T, H):
+    """Fills a MoeNorm's gate from a number or a tensor that broadcasts to [T, H]."""
+    if isinstance(gate, (int, float)):
+        n.gate_scale = gate
+        return
+    _on(gate, "gate", dev)
+    n.gate_type = _type(gate, "gate")
+    try:
+        g = gate.expand(T, H)
+    except RuntimeError:
+        raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}") from None
+    st, sh = g.stride()
+    if H == 1:
+        sh = 0
+    if sh not in (0, 1):
+        raise ValueError("gate must be contiguous or broadcast along H")
+    n.gate, n.gate_stride_t, n.gate_stride_h = g.data_ptr(), st if T > 1 else 0, sh
+
+
 def _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_scale, pre_norm, pre_weight,
                weight_offset, eps):
     """Fills everything of a MoeNorm but its outputs and y; returns the normed flag."""
@@ -112,8 +132,7 @@ def _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_sc
     n.gate_scale = 1.0
     if residual is not None:
         n.stream_type = _type(residual, "residual")
-        n.residual_stride = _rows(residual, "residual", dev, T, H)
-        n.residual = residual.data_ptr()
+        n.residual_stride, n.residual = _rows(residual, "residual", dev, T, H), residual.data_ptr()
     if post_norm or post_weight is not None:
         n.flags = MOE_N_POST
     for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
@@ -123,21 +142,7 @@ def _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_sc
     if post_weight is not None and pre_weight is not None and post_weight.dtype != pre_weight.dtype:
         raise ValueError("post_weight and pre_weight must have the same type")
     if gate is not None:
-        if isinstance(gate, (int, float)):
-            n.gate_scale = gate
-        else:
-            _on(gate, "gate", dev)
-            n.gate_type = _type(gate, "gate")
-            try:
-                g = gate.expand(T, H)
-            except RuntimeError:
-                raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}") from None
-            st, sh = g.stride()
-            if H == 1:
-                sh = 0
-            if sh not in (0, 1):
-                raise ValueError("gate must be contiguous or broadcast along H")
-            n.gate, n.gate_stride_t, n.gate_stride_h = g.data_ptr(), st if T > 1 else 0, sh
+        _gate(n, gate, dev, T, H)
     return pre_norm or pre_weight is not None
 
 
@@ -266,3 +271,152 @@ def router_forward(x, weight, k, *, norm=True, eps=1e-6, expert_scale=None, logi
         return lo, i, w
 
     return _call(dev, stream, go)
+
+
+class MoeLayerDesc(ctypes.Structure):
+    _fields_ = [("flags", ctypes.c_uint32), ("router_flags", ctypes.c_uint32), ("norm_type", ctypes.c_int32),
+                ("router_type", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)] + \
+               [(n, ctypes.c_void_p) for n in
+                ("norm_weight", "router_weight", "expert_scale", "w_gateup", "s_gateup", "b_gateup", "w_down",
+                 "s_down", "b_down", "topk_ids", "topk_weights")]
+
+
+class MoeLayer:
+    """A whole mixture-of-experts layer over fixed weights:
+
+        n   = rms(x) * (weight_offset + norm_weight)             (norm=False: n = x)
+        ids, w = router_forward(x, router_weight, k, norm=router_norm, expert_scale=...)
+        y   = sum_j w_j FFN of expert ids_j on n                 (expert_ffn_forward)
+        out, normed = block_norm(y, residual, post_weight=..., gate=..., pre_weight=..., ...)
+
+    Weights as for router_forward and expert_ffn_forward; norm_weight, post_weight
+    and pre_weight are [H] in bf16 or fp32 (post and pre alike; pre_norm=True or
+    post_norm=True without a weight norms by ones).  The handle checks them once and
+    keeps them alive; it holds no other state, so calls on several streams are
+    independent as long as each has a workspace of its own.
+
+    Calls of up to 16 tokens take two launches."""
+
+    FEW_TOKENS = 16
+
+    def __init__(self, router_weight, k, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, *, norm=True,
+                 norm_weight=None, router_norm=True, expert_scale=None, post_norm=False, post_weight=None,
+                 pre_norm=False, pre_weight=None, weight_offset=0.0, swiglu=False, fp32_intermediate=False, eps=1e-6):
+        import torch
+        bgq = _api()
+        dev = self.device = _device(router_weight, "router_weight")
+        if router_weight.dim() != 2 or not router_weight.is_contiguous():
+            raise ValueError("router_weight must be a contiguous [E, H] tensor")
+        E, H = router_weight.shape
+        if w_gateup.dim() != 3 or w_gateup.shape[0] != E or w_gateup.shape[1] % 2:
+            raise ValueError(f"w_gateup has shape {tuple(w_gateup.shape)}, expected ({E}, 2 I, words)")
+        I = w_gateup.shape[1] // 2
+        bits = w_gateup.shape[2] * 32 // H
+        if bits not in (4, 8) or w_gateup.shape[2] * 32 != bits * H:
+            raise ValueError(f"w_gateup has {w_gateup.shape[2]} words per row: neither 4-bit nor 8-bit codes of H={H}")
+        ng = s_gateup.shape[-1]
+        if ng < 1 or H % ng:
+            raise ValueError(f"s_gateup has {ng} groups per row, which does not divide H={H}")
+        gs = H // ng
+        if not 1 <= k <= min(E, 64):
+            raise ValueError(f"k must be between 1 and min(E, 64) = {min(E, 64)}, got {k}")
+        d = self._desc = MoeLayerDesc()
+        for name, t, size, shape in (("w_gateup", w_gateup, 4, (E, 2 * I, H * bits // 32)),
+                                     ("s_gateup", s_gateup, 2, (E, 2 * I, ng)), ("b_gateup", b_gateup, 2, (E, 2 * I, ng)),
+                                     ("w_down", w_down, 4, (E, H, I * bits // 32)),
+                                     ("s_down", s_down, 2, (E, H, I // gs)), ("b_down", b_down, 2, (E, H, I // gs))):
+            _on(t, name, dev)
+            setattr(d, name, bgq._dev_ptr(t, name, size, shape).value)
+        d.flags = 1 if norm else 0
+        d.router_flags = MOE_R_NORM if router_norm else 0
+        d.eps, d.weight_offset = eps, weight_offset
+        d.router_weight, d.router_type = router_weight.data_ptr(), _type(router_weight, "router_weight")
+        if norm_weight is not None:
+            if not norm:
+                raise ValueError("norm_weight is given with norm=False")
+            d.norm_weight, d.norm_type = _vector(norm_weight, "norm_weight", dev, H), _type(norm_weight, "norm_weight")
+        if expert_scale is not None:
+            if expert_scale.dtype is not torch.float32:
+                raise ValueError(f"expert_scale must be float32, got {expert_scale.dtype}")
+            d.expert_scale = _vector(expert_scale, "expert_scale", dev, E)
+        self.E, self.H, self.I, self.k, self.group_size, self.bits = E, H, I, k, gs, bits
+        self.eps, self.weight_offset = eps, weight_offset
+        self._tail = MoeNorm()
+        self._pre = _norm_tail(self._tail, 0, H, dev, None, post_norm, post_weight, None, 1.0, pre_norm, pre_weight,
+                               weight_offset, eps)
+        self._flags = (bgq.MOE_F_SWIGLU if swiglu else 0) | (bgq.MOE_F_FP32_INTERMEDIATE if fp32_intermediate else 0)
+        self._keep = (router_weight, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, norm_weight, expert_scale,
+                      post_weight, pre_weight)
+        if self.workspace_bytes(1) == 0:
+            raise ValueError(f"unsupported layer: E={E}, H={H}, I={I}, k={k}, group size {gs}, {bits} bits")
+
+    def _problem(self, T):
+        return _api().problem(T, self.k, self.E, self.H, self.I, self._flags, group_size=self.group_size, bits=self.bits)
+
+    def workspace_bytes(self, T):
+        """Bytes of device workspace a call on T tokens needs (0: unsupported)."""
+        return int(_api().lib().moe_layer_workspace_bytes(ctypes.byref(self._problem(T))))
+
+    def __call__(self, x, *, residual=None, gate=None, residual_scale=1.0, out=None, normed=None, ids=None, weights=None,
+                 workspace=None, stream=None):
+        """The layer on x bf16 [T, H].  residual, gate and residual_scale as for
+        block_norm (rows of residual, out, normed and a [T, H] gate start on 16
+        bytes); out and normed default to the residual's type (x's without one).  ids
+        (int32) and weights (fp32), [T, k], receive the routing if given.  workspace:
+        a uint8 tensor of workspace_bytes(T) bytes, one per call at a time (allocated
+        if None).  Returns out, or (out, normed) if the layer norms its output."""
+        import torch
+        bgq = _api()
+        dev, H, k = self.device, self.H, self.k
+        if x.dim() != 2 or x.shape[1] != H or x.dtype is not torch.bfloat16 or not x.is_contiguous():
+            raise ValueError(f"x must be a contiguous bfloat16 [T, {H}] tensor")
+        _on(x, "x", dev)
+        T = x.shape[0]
+        p = self._problem(T)
+        n = MoeNorm.from_buffer_copy(self._tail)
+        n.T = T
+        dtype = x.dtype if residual is None else residual.dtype
+        n.residual_scale = residual_scale
+        if residual is not None:
+            n.stream_type = _type(residual, "residual")
+            n.residual_stride, n.residual = _rows(residual, "residual", dev, T, H), residual.data_ptr()
+        elif out is not None:
+            n.stream_type, dtype = _type(out, "out"), out.dtype
+        if out is not None and out.dtype is not dtype:
+            raise ValueError(f"out must have the residual's type {dtype}, got {out.dtype}")
+        if gate is not None:
+            _gate(n, gate, dev, T, H)
+        if normed is not None and not self._pre:
+            raise ValueError("normed is given, but the layer has no norm after it")
+        desc = self._desc
+        if ids is not None or weights is not None:
+            desc = MoeLayerDesc.from_buffer_copy(desc)
+            if ids is not None:
+                desc.topk_ids = _output(ids, "ids", dev, (T, k), torch.int32)
+            if weights is not None:
+                desc.topk_weights = _output(weights, "weights", dev, (T, k), torch.float32)
+
+        def go(raw):
+            o, m, ws = out, normed, workspace
+            if o is None:
+                o = torch.empty((T, H), dtype=dtype, device=dev)
+            n.out_stride, n.out = _rows(o, "out", dev, T, H), o.data_ptr()
+            if self._pre:
+                if m is None:
+                    m = torch.empty((T, H), dtype=dtype, device=dev)
+                n.normed_type = _type(m, "normed")
+                n.normed_stride, n.normed = _rows(m, "normed", dev, T, H), m.data_ptr()
+            if ws is None:
+                need = bgq.lib().moe_layer_workspace_bytes(ctypes.byref(p))
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+            else:
+                _on(ws, "workspace", dev)
+                if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+                    raise ValueError("workspace must be a contiguous uint8 tensor")
+            st = bgq.lib().moe_layer_forward(ctypes.byref(p), ctypes.byref(desc), x.data_ptr(), ctypes.byref(n),
+                                             ws.data_ptr(), ws.numel(), raw)
+            if st != 0:
+                raise bgq.MoeError(st, "moe_layer_forward")
+            return (o, m) if self._pre else o
+
+        return _call(dev, stream, go)

@@ -420,6 +420,55 @@ typedef struct {
 moe_status moe_router_forward(const moe_router* r, const void* x, float* logits, int32_t* topk_ids,
                               float* topk_weights, void* stream);
 
+/*
+ * A whole mixture-of-experts layer:
+ *
+ *   n   = rms(x) * (weight_offset + norm_weight)    with MOE_L_NORM, else n = x
+ *   ids, w : the router of x (moe_router_forward with router_flags, router_weight,
+ *         router_type, expert_scale and eps)
+ *   y   = sum_j w_j FFN of expert ids_j on n        (moe_expert_ffn_forward)
+ *   out, normed : moe_block_norm of y with `tail`
+ *
+ * Up to MOE_LAYER_FEW_TOKENS tokens run in two launches, with n and the product
+ * h kept to 16 significant bits (bf16 hi + lo); larger batches run the operators
+ * one after the other, n in bf16 and h in bf16 unless MOE_F_FP32_INTERMEDIATE.
+ * y is fp32 either way.  Results are deterministic; a token's differ within these
+ * roundings with the number of tokens in the batch.
+ */
+#define MOE_LAYER_FEW_TOKENS 16
+#define MOE_L_NORM 1u
+typedef struct {
+    uint32_t flags;            /* MOE_L_*                                            */
+    uint32_t router_flags;     /* MOE_R_*                                            */
+    int32_t norm_type;         /* MOE_T_* of norm_weight                             */
+    int32_t router_type;       /* MOE_T_* of router_weight                           */
+    float eps;                 /* of n and of the router, >= 0                       */
+    float weight_offset;
+    const void* norm_weight;   /* [H] or NULL (weight 1, offset unused); 16-byte aligned */
+    const void* router_weight; /* [E, H], 16-byte aligned                            */
+    const float* expert_scale; /* [E] or NULL                                        */
+    const uint32_t* w_gateup;  /* the experts, as for moe_expert_ffn_forward         */
+    const void* s_gateup;
+    const void* b_gateup;
+    const uint32_t* w_down;
+    const void* s_down;
+    const void* b_down;
+    int32_t* topk_ids;         /* out: int32 [T, k], or NULL                         */
+    float* topk_weights;       /* out: fp32 [T, k], or NULL                          */
+} moe_layer;
+
+/* Device workspace of moe_layer_forward (0 on an invalid p). */
+size_t moe_layer_workspace_bytes(const moe_problem* p);
+
+/* p as for moe_expert_ffn_forward, without MOE_F_FP32_OUT and with k <= 64; x bf16
+ * [T, H], 16-byte aligned.  tail: T and H as in p, y_type and y_stride are not
+ * used; every row of its tensors starts on 16 bytes; out may be x or the residual
+ * itself (same type and row stride).  ws: moe_layer_workspace_bytes(p) bytes,
+ * 256-byte aligned, with any contents; one call at a time may use it (calls, or
+ * captured graphs, that share one must be ordered by the caller). */
+moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const void* x, const moe_norm* tail,
+                             void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status s);
 
