@@ -334,7 +334,7 @@ LayerLayout layer_layout(const moe_problem* p) {
     l.few = p->T <= MOE_LAYER_FEW_TOKENS;
     l.logits = take(4 * T * p->E);
     if (l.few) {
-        l.num_counters = static_cast<int32_t>(2 * moe::kLayerRanges + moe::kLayerFewTokens + 2 * A + 1);
+        l.num_counters = static_cast<int32_t>(2 * moe::kLayerRanges + 2 * moe::kLayerCounterStride * A + 1);
         l.counters = take(4 * static_cast<size_t>(l.num_counters));
         l.n = take(4 * T * H);
         l.nsum = take(8 * T * (H / 32));
@@ -422,6 +422,8 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
         a.norm_f32 = l->norm_type == MOE_T_FP32;
         a.eps = l->eps;
         a.weight_offset = l->weight_offset;
+        a.magic_gateup = static_cast<uint32_t>(((1ull << 32) + p->I / 16 - 1) / (p->I / 16));
+        a.magic_down = static_cast<uint32_t>(((1ull << 32) + p->H / 32 - 1) / (p->H / 32));
         a.router = router_args(&r, x, logits);
         a.expert_scale = l->expert_scale;
         a.x = static_cast<const uint16_t*>(x);
@@ -440,10 +442,9 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
         a.num_counters = y.num_counters;
         a.claim_gateup = a.counters;
         a.claim_down = a.claim_gateup + moe::kLayerRanges;
-        a.claim_token = a.claim_down + moe::kLayerRanges;
-        a.done_gateup = a.claim_token + moe::kLayerFewTokens;
-        a.done_down = a.done_gateup + A;
-        a.failed = a.done_down + A;
+        a.done_gateup = a.claim_down + moe::kLayerRanges;
+        a.done_down = a.done_gateup + moe::kLayerCounterStride * A;
+        a.failed = a.done_down + moe::kLayerCounterStride * A;
         a.logits = logits;
         a.n = reinterpret_cast<uint16_t*>(base + y.n);
         a.nsum = reinterpret_cast<float*>(base + y.nsum);

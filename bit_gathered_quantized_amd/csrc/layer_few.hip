@@ -2,8 +2,8 @@
 //
 //   1. moe_layer_few_route: logits = rstd (x . Wr^T), one workgroup an expert;
 //      n = rms(x) w, one workgroup a token, as bf16 hi + lo (16 bits) in the order
-//      of the matmul operand, with its sums over chains of columns; the second
-//      launch's counters are cleared.
+//      of the matmul operand, with its sums over groups; the second launch's
+//      counters are cleared.
 //   2. moe_layer_few_experts: top-k in every workgroup (it is cheaper than a wait),
 //      gate|up with the activation, down, and per token the weighted sum over its
 //      experts with the norms and the residual around it.
@@ -16,8 +16,11 @@
 // Tiles.  An expert's rows go in tiles of at most 8: a 16-row MFMA operand holds
 // the hi parts of 8 rows and their lo parts below, so 16-bit activations cost no
 // MFMA more than 8-bit ones, and the two halves of a product are added at its end.
-// The codes are exact operands (OFF + q); with P = x . (OFF + q) - OFF X over a
-// chain of columns, X the chain's sum of x, the accumulator takes s P + b X.
+// The codes are exact operands (OFF + q).  With P = x . (OFF + q) over a group of
+// columns and X the group's sum of x, the accumulator takes s P per group, and
+// sum_g b X - s OFF X once per unit on MFMAs: a wave's slice has at most 8 groups
+// (16 of 32 columns), s and b are bf16 as they are, and X goes in as three bf16
+// parts in three of the four 8-value pieces of K, exact to its last bit.
 //
 // A unit is 32 weight rows (gate|up: 16 columns of h, both halves; down: 32
 // output columns) by all of K, cut over SPLIT waves that hold at most 4 chunks of
@@ -26,12 +29,12 @@
 // workgroup b takes the b-th of 256 equal ranges of them.
 //
 // Order between the phases without a barrier.  A range is taken by an exchange on
-// its own flag.  A workgroup takes its own range, then any range that it finds
-// untaken, and only when all ranges of a phase are taken does it go on to the
-// next phase, where it may wait for counters (units done per tile).  So whoever
-// waits waits for running workgroups of an earlier phase, and the first phase
-// waits for nobody: every wait ends, however few workgroups the GPU holds at
-// once.  (Waits are also bounded: a workspace that another call writes to gives
+// its own flag.  A workgroup takes its own range of both matmuls when it starts,
+// then, at the end of a phase, any range of it that is still untaken, and only
+// when all ranges of a phase are taken does it wait for the counters (units done
+// per tile) of that phase; workgroup t finishes token t at last.  So whoever waits waits for running workgroups, for
+// ranges of an earlier phase than its own, and the first phase waits for nobody:
+// every wait ends, however few workgroups the GPU holds at once.  (Waits are also bounded: a workspace that another call writes to gives
 // NaN, not a hang.)
 //
 // What one workgroup writes and another reads within the launch (h and its sums,
@@ -53,10 +56,8 @@ constexpr int kTileRows = 8;
 constexpr int kMaxSlots = kLayerFewTokens * kRouterMaxK;  // assignments, and so tiles
 constexpr int kChunks = 4;                                // chunks of 128 columns a wave holds
 constexpr int kSc1 = 16;                                  // buffer access past the XCD's L2
+constexpr int kPad = kLayerCounterStride;                 // counters lie on cache lines of their own
 constexpr int kSpinLimit = 1 << 22;                       // polls of about 1 us
-
-template <int GS>
-constexpr int kChainCols = Geo<GS>::kChain;
 
 // ------------------------------------------------------------ first launch
 template <int TM>
@@ -96,9 +97,9 @@ __global__ __launch_bounds__(256) void moe_layer_few_route(LayerArgs a) {
             ss = fmaf(v[i][j], v[i][j], ss);
         }
     const float rstd = a.norm ? 1.f / sqrtf(norm::row_sum<4>(ss, part[0][0]) / H + a.eps) : 1.f;
-    const int chain = a.gs == 32 ? 32 : 64, per = chain / 8;  // threads of a chain
+    const int gs = a.gs, per = gs / 8;  // threads of a group
     uint16_t* const n = a.n + static_cast<size_t>(2 * t) * H;
-    float* const sums = a.nsum + static_cast<size_t>(2 * t) * (H / chain);
+    float* const sums = a.nsum + static_cast<size_t>(2 * t) * (H / gs);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int c = 8 * (threadIdx.x + 256 * i);
@@ -125,9 +126,9 @@ __global__ __launch_bounds__(256) void moe_layer_few_route(LayerArgs a) {
         if (c < H) {
             *reinterpret_cast<u32x4*>(n + c) = u32x4{hi[0], hi[1], hi[2], hi[3]};
             *reinterpret_cast<u32x4*>(n + H + c) = u32x4{lo[0], lo[1], lo[2], lo[3]};
-            if (c % chain == 0) {
-                sums[c / chain] = shi;
-                sums[H / chain + c / chain] = slo;
+            if (c % gs == 0) {
+                sums[c / gs] = shi;
+                sums[H / gs + c / gs] = slo;
             }
         }
     }
@@ -137,18 +138,30 @@ __global__ __launch_bounds__(256) void moe_layer_few_route(LayerArgs a) {
 // The lists that every workgroup makes of the chosen experts.
 struct Lists {
     int32_t tiles;                             // tiles in all
-    uint16_t rows[kMaxSlots][kTileRows];       // assignments t * k + j of a tile's rows
+    uint16_t rows[kMaxSlots][kTileRows];       // 64 t + j of a tile's rows
     uint16_t expert[kMaxSlots];                // a tile's expert
     uint8_t count[kMaxSlots];                  // and its rows
     uint16_t slot_tile[kMaxSlots];             // the tile of an assignment
     float weight[kMaxSlots];                   // its routing weight
 };
 
+// Chunks that a wave turns at a time: all of a unit with 4-bit codes, half of it
+// with 8-bit ones (LDS).
+template <int BITS>
+constexpr int kBuffers = BITS == 4 ? kChunks : kChunks / 2;
+
+// 16-byte pieces of scales (or biases) of the units at work per thread of half a
+// workgroup: units times columns are at most 4096.
+template <int GS>
+constexpr int kTablePieces = 4 * 4096 / GS / (kFewThreads / 2) > 0 ? 4 * 4096 / GS / (kFewThreads / 2) : 1;
+
+// A row of nch chunks is cut over 1 << split_log waves.
+__device__ __forceinline__ int split_log(int nch) { return nch <= 4 ? 0 : nch <= 8 ? 1 : nch <= 16 ? 2 : 3; }
+
 template <int GS, int BITS>
 struct alignas(16) FewSmem {
-    uint32_t w[kWaves][2 * 16 * 4 * BITS];          // weight transposition, a wave's own
-    uint16_t tables[2][8 * 4096 / GS * 8];          // scales and biases of the units at work, of the next ones
-    float xs[kWaves][kChunks * Geo<GS>::kChains][16];  // chain sums of a wave's slice, per operand row
+    uint32_t w[kWaves][kBuffers<BITS>][2 * 16 * 4 * BITS];  // weight transposition, a wave's own
+    uint16_t tables[2][2][kTablePieces<GS> * kFewThreads / 2 * 8];  // scales, biases of the units at work, of the next ones
     float red[2][kWaves][2][kTileRows][16];         // the waves' shares of the units' outputs
     union {
         struct {
@@ -159,7 +172,7 @@ struct alignas(16) FewSmem {
         };
         float lds[2][16];                       // sums of the last phase
     };
-    int32_t pick;
+    int32_t pick, own[2];
     Lists l;
 };
 
@@ -179,29 +192,24 @@ __device__ __forceinline__ void give_up(const LayerArgs& a) {
     __hip_atomic_store(a.failed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Takes flag `own`, or with own < 0 any untaken one of n <= kFewThreads flags; -1
-// once all are taken.  Called by the whole workgroup.
+// Takes any untaken one of n <= kFewThreads flags; -1 once all are taken.  Called
+// by the whole workgroup.
 template <class Smem>
-__device__ __forceinline__ int take(Smem& sm, int32_t* flags, int n, int own) {
+__device__ __forceinline__ int take(Smem& sm, int32_t* flags, int n) {
     for (;;) {
         __syncthreads();
-        if (threadIdx.x == 0) sm.pick = own >= 0 ? own : INT32_MAX;
+        if (threadIdx.x == 0) sm.pick = INT32_MAX;
         __syncthreads();
-        if (own < 0) {
-            const int i = threadIdx.x;
-            if (i < n && !__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
-                atomicMin(&sm.pick, i);
-            __syncthreads();
-            if (sm.pick == INT32_MAX) return -1;
-        }
-        if (threadIdx.x == 0) {
-            const int i = sm.pick;
-            if (__hip_atomic_exchange(flags + i, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) sm.pick = -1;
-        }
+        const int i = threadIdx.x;
+        if (i < n && !__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMin(&sm.pick, i);
         __syncthreads();
-        const int got = sm.pick;
-        if (got >= 0) return got;
-        own = -1;  // another workgroup was first: look for what is left
+        const int want = sm.pick;
+        if (want == INT32_MAX) return -1;
+        __syncthreads();
+        if (threadIdx.x == 0 && __hip_atomic_exchange(flags + want, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+            sm.pick = -1;  // another workgroup was first: look again
+        __syncthreads();
+        if (sm.pick >= 0) return want;
     }
 }
 
@@ -210,6 +218,10 @@ template <class Smem>
 __device__ __forceinline__ void make_lists(const LayerArgs& a, Smem& sm) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int T = a.T, k = a.k, E = a.E;
+    // the last wave (the first ones have a token each) takes the workgroup's ranges
+    if (wave == kWaves - 1 && lane < 2)
+        sm.own[lane] = !__hip_atomic_exchange((lane ? a.claim_down : a.claim_gateup) + blockIdx.x, 1, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
     for (int e = threadIdx.x; e < E; e += kFewThreads) sm.mask[e] = 0;
     for (int t = wave; t < T; t += kWaves) {
         const float* row = a.logits + static_cast<size_t>(t) * E;
@@ -258,7 +270,7 @@ __device__ __forceinline__ void make_lists(const LayerArgs& a, Smem& sm) {
         const int e = sm.id[s], t = s / k;
         const uint32_t m = sm.mask[e];
         const int rank = __popc(m & ((1u << t) - 1u)), tile = sm.base[e] + rank / kTileRows;
-        sm.l.rows[tile][rank % kTileRows] = static_cast<uint16_t>(s);
+        sm.l.rows[tile][rank % kTileRows] = static_cast<uint16_t>(64 * t + s - t * k);
         sm.l.slot_tile[s] = static_cast<uint16_t>(tile);
         if (rank % kTileRows == 0) {
             sm.l.expert[tile] = static_cast<uint16_t>(e);
@@ -268,190 +280,319 @@ __device__ __forceinline__ void make_lists(const LayerArgs& a, Smem& sm) {
     __syncthreads();
 }
 
-// One phase (kDown: the down matmul, else gate|up) of one range of units.
-template <int GS, int BITS, bool kDown>
-__device__ __forceinline__ void run_range(const LayerArgs& a, FewSmem<GS, BITS>& sm, int range) {
-    constexpr int CH = Geo<GS>::kChains, MPG = Geo<GS>::kSlices, SH = Geo<GS>::kShift;
+// The sums over groups g0 .. g0 + 7 of one operand row, those from the n-th on
+// zeros.  gate|up: from n's group sums; down: from h's sums over 16 columns.  `at`
+// is the byte offset of group g0's.
+template <int GS, bool kDown>
+__device__ __forceinline__ void load_sums(float (&v)[8], Rsrc all, uint32_t at, int n) {
+    constexpr int B = kDown ? GS / 16 : 1;  // floats of a group
+    const Rsrc none = make_rsrc(nullptr, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const Rsrc r = j < n ? all : none;
+        const uint32_t o = at + 4 * B * j;
+        if constexpr (B == 1) {
+            v[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
+        } else if constexpr (B == 2) {
+            const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, o, 0, kSc1));
+            v[j] = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+        } else {
+            float sum = 0.f;
+#pragma unroll
+            for (int h = 0; h < B / 4; ++h) {
+                const f32x4 b = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, o + 16 * h, 0, kSc1));
+                sum = (((sum + b[0]) + b[1]) + b[2]) + b[3];
+            }
+            v[j] = sum;
+        }
+    }
+}
+
+// A value that is the same in every lane, as a scalar (one read from LDS is not
+// known to be).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// v as a value that the compiler forms anew here: what follows from it is computed
+// where it is used, not kept in registers through the loop.
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
+// Waits until all loads of the wave have returned.  The compiler tracks loads per
+// register over branches: one that may still be under way on one side of a branch
+// makes every later use wait for whatever was issued since.
+__device__ __forceinline__ void loads_done() { __builtin_amdgcn_s_waitcnt(0x0F70); }  // vmcnt(0)
+
+// One phase (kDown: the down matmul, else gate|up) of one range of units; a wave's
+// slice is CPW chunks of 128 columns (the last of a row may be missing: zeros).
+// Returns whether `flags`, the phase's, still hold an untaken range.
+//
+// The loop over units has no branch around a load: what does not exist (a chunk
+// past the row, a unit past the range) is read through an empty resource.
+template <int GS, int BITS, bool kDown, int CPW>
+__device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>& sm, int any_range, const int32_t* flags) {
+    const int range = uniform(any_range);
+    constexpr int CH = Geo<GS>::kChains, SH = Geo<GS>::kShift;
     constexpr int OFF = kCodeOffset<BITS, true>;
+    constexpr int NS = (CPW * 128 / GS + 7) / 8;  // bias steps of a wave's slice
+    constexpr int NP = kTablePieces<GS>;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, lr = lane & 15;
-    const int K = kDown ? a.I : a.H, G = K / GS, row_words = K / 32 * BITS, chains = K / kChainCols<GS>;
+    const int K = kDown ? a.I : a.H, G = K / GS, row_words = K / 32 * BITS;
+    const int rows_e = kDown ? a.H : 2 * a.I;     // weight rows of an expert
     const int upt = kDown ? a.H / 32 : a.I / 16;  // units of a tile
     const int nch = (K + 127) / 128;
-    const int log_split = nch <= 4 ? 0 : nch <= 8 ? 1 : nch <= 16 ? 2 : 3, split = 1 << log_split;
+    const int log_split = split_log(nch), split = 1 << log_split;
     const int nu = kWaves >> log_split;           // units at work at a time
     const int wu = wave >> log_split, ws = wave & (split - 1);
-    const int ch0 = nch * ws >> log_split, nc = (nch * (ws + 1) >> log_split) - ch0;  // this wave's chunks, <= 4
-    const int N = sm.l.tiles * upt, groups = kRanges * nu;
-    auto first = [&](int g) { return static_cast<int>(static_cast<int64_t>(N) * g / groups); };
-    const int lo = first(range * nu), hi = first((range + 1) * nu);
-    if (lo == hi) return;
-    const int u0 = first(range * nu + wu), u1 = first(range * nu + wu + 1);
+    const int ch0 = nch * ws >> log_split, nc = (nch * (ws + 1) >> log_split) - ch0;  // this wave's chunks, <= CPW
+    const int N = uniform(sm.l.tiles) * upt, shift = 8 + 3 - log_split;  // kRanges * nu shares, N share < 2^30
+    static_assert(kRanges == 1 << 8 && kWaves == 1 << 3, "shift");
+    auto first = [&](int share) { return N * share >> shift; };
+    const int r0 = range * nu, lo = first(r0), hi = first(r0 + nu);
+    const int u0 = first(r0 + wu), u1 = first(r0 + wu + 1);
+    // the shares of a range differ by one unit at most
     int steps = 0;
-    for (int i = 0; i < nu; ++i) steps = max(steps, first(range * nu + i + 1) - first(range * nu + i));
+    for (int i = 0; i < nu; ++i) steps = max(steps, first(r0 + i + 1) - first(r0 + i));
 
-    const uint32_t* const w = kDown ? a.w_d : a.w_gu;
-    const uint16_t* const s16 = kDown ? a.s_d : a.s_gu;
-    const uint16_t* const b16 = kDown ? a.b_d : a.b_gu;
+    // u / upt for u < 2^18, upt <= 256: u (m upt - 2^32) < 2^26 errs by less than 1 / upt
+    const uint32_t magic = kDown ? a.magic_down : a.magic_gateup;
+    auto tile_of = [&](int u) { return static_cast<int>(__umulhi(static_cast<uint32_t>(u), magic)); };
     // the first weight row of block b of unit u
     auto row_of = [&](int u, int b) {
-        const int tile = u / upt, i = u - tile * upt;
-        const size_t e = sm.l.expert[tile];
-        return kDown ? e * a.H + 32 * i + 16 * b : e * 2 * a.I + 16 * i + (b ? a.I : 0);
+        const int tile = tile_of(u), i = u - tile * upt;
+        const uint32_t e = sm.l.expert[tile];
+        return e * rows_e + (kDown ? 32 * i + 16 * b : 16 * i + (b ? a.I : 0));
     };
     WaveW<2, GS, BITS> ww;
-    auto aim = [&](int u) {  // ww loads unit u from now on
+    // ww loads unit u from now on, or nothing from u1 on
+    auto aim = [&](int u) {
+        const uint32_t* const w = kDown ? a.w_d : a.w_gu;
         const uint32_t* blk[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const size_t r = row_of(u, b);
-            const uint32_t rl = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(r)),
-                           rh = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(r >> 32));
-            blk[b] = w + ((static_cast<size_t>(rh) << 32 | rl)) * row_words;
+            const uint32_t r = uniform(row_of(min(u, u1 - 1), b));
+            blk[b] = w + static_cast<size_t>(r) * row_words;
         }
-        ww.init(sm.w[wave], blk, row_words);
+        ww.init(sm.w[wave][0], blk, row_words);
+        if (u >= u1) ww.blk[0] = ww.blk[1] = make_rsrc(w, 0);
     };
-    u32x4 rv[kChunks][2][BITS / 4];
-    if (u0 < u1) {
-        aim(u0);
+    // Tables: the scales of the units at work, then their biases, 2 G pieces of 16
+    // bytes a block of 16 rows.  The first half of the workgroup loads scales, the
+    // other biases, NP pieces a thread.
+    constexpr int kHalf = kFewThreads / 2;
+    const bool biases = wave >= kWaves / 2;
+    const uint16_t* const tab = kDown ? (biases ? a.b_d : a.s_d) : (biases ? a.b_gu : a.s_gu);
+    const Rsrc rt = make_rsrc(tab, 2u * a.E * rows_e * G);
+    int tu[NP];        // a piece's unit, its block and its place in the block
+    uint32_t tblk[NP], tat[NP];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-            if (i < nc) ww.load(ch0 + i, rv[i]);
+    for (int h = 0; h < NP; ++h) {
+        const int p = (tid & (kHalf - 1)) + kHalf * h, i = p / (4 * G), r = p - i * 4 * G;
+        tu[h] = i;
+        tblk[h] = r / (2 * G);
+        tat[h] = 16 * (r - tblk[h] * 2 * G);
     }
-    // tables: per unit the scales and then the biases of its 2 x 16 rows, 2 G
-    // pieces of 16 bytes a block; at most 2 pieces a thread
-    u32x4 tv[2];
+    u32x4 tv[NP];
     auto load_tables = [&](int step) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = tid + kFewThreads * h, i = p / (8 * G), r = p - i * 8 * G, seg = r / (2 * G), at = r - seg * 2 * G;
-            const int u = first(range * nu + min(i, nu - 1)) + step;
-            if (i < nu && u < first(range * nu + i + 1))
-                tv[h] = *reinterpret_cast<const u32x4*>((seg < 2 ? s16 : b16) + row_of(u, seg & 1) * G + 8 * at);
+        for (int h = 0; h < NP; ++h) {
+            const int u = first(r0 + tu[h]) + step, end = first(r0 + tu[h] + 1);
+            const uint32_t at = 2u * G * row_of(max(min(u, end - 1), 0), tblk[h]) + tat[h];
+            tv[h] = load16(rt, tu[h] < nu && u < end ? at : 0xFFFFFFF0u, 0);
         }
     };
     auto store_tables = [&](int step) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = tid + kFewThreads * h;
-            if (p < nu * 8 * G) *reinterpret_cast<u32x4*>(sm.tables[step & 1] + 8 * p) = tv[h];
+        for (int h = 0; h < NP; ++h)
+            *reinterpret_cast<u32x4*>(sm.tables[step & 1][biases] + 8 * ((tid & (kHalf - 1)) + kHalf * h)) = tv[h];
+    };
+
+    // a tile's activations for this wave's slice: operand row lr is part lr / 8 of
+    // the tile's row lr % 8; rows past the tile and columns past K are zeros
+    const uint32_t slots = static_cast<uint32_t>(kDown ? a.T * a.k : a.T);
+    const Rsrc rx = make_rsrc(kDown ? a.h : a.n, 4u * K * slots);
+    const Rsrc rs = kDown ? make_rsrc(a.hsum, 8u * (K / 16) * slots) : make_rsrc(a.nsum, 8u * G * slots);
+    const Rsrc none = make_rsrc(a.n, 0);
+    u32x4 x[CPW][4], xb[NS], xo[NS];
+    float sums[NS][8];
+    const int g0 = ch0 * 128 / GS, ng = min(nc * 128 / GS, G - g0);  // the slice's groups
+    const int cols = min(nc * 128, K - 128 * ch0);                   // and columns
+    auto load_x = [&](int tile) {
+        const int ng_ = fresh(ng), cols_ = fresh(cols);
+        const int count = sm.l.count[tile], r = lr & 7;
+        const int slot = sm.l.rows[tile][min(r, count - 1)];
+        const uint32_t src = 2u * static_cast<uint32_t>(kDown ? (slot >> 6) * a.k + (slot & 63) : slot >> 6) + (lr >> 3);
+        // rows past the tile lie past every resource
+        const bool mine = r < count;
+        constexpr int B = kDown ? GS / 16 : 1;
+#pragma unroll
+        for (int st = 0; st < NS; ++st)
+            load_sums<GS, kDown>(sums[st], rs, mine ? 4u * B * (src * G + g0 + 8 * st) : 0xFFFFF000u, ng_ - 8 * st);
+        const uint32_t base = mine ? 2u * (K * src + 128 * ch0 + (Geo<GS>::kChain == 64 ? 16 : 8) * q) : 0xFFFFF000u;
+#pragma unroll
+        for (int i = 0; i < CPW; ++i)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const Rsrc rh = 128 * i + 64 * half < cols_ ? rx : none;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    x[i][2 * half + s] = __builtin_bit_cast(
+                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                   rh, base + 256 * i + 128 * half + (Geo<GS>::kChain == 64 ? 16 : 64) * s, 0, kDown ? kSc1 : 0));
+            }
+    };
+    // lane (lr, q) brings part q of the sums of row lr: X = hi + mid + lo
+    auto split_sums = [&] {
+#pragma unroll
+        for (int st = 0; st < NS; ++st) {
+            xb[st] = u32x4{0, 0, 0, 0};
+            xo[st] = xb[st];
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t pk = pack_bf16x2(sums[st][2 * j], sums[st][2 * j + 1]);
+                    const float p0 = __uint_as_float(pk << 16), p1 = __uint_as_float(pk & 0xFFFF0000u);
+                    sums[st][2 * j] -= p0;
+                    sums[st][2 * j + 1] -= p1;
+                    const uint32_t off = pack_bf16x2(-static_cast<float>(OFF) * p0, -static_cast<float>(OFF) * p1);
+                    xb[st][j] = q == part ? pk : xb[st][j];
+                    xo[st][j] = q == part ? off : xo[st][j];
+                }
         }
     };
-    load_tables(0);
-    store_tables(0);
+    // eight entries of a table row, those past the slice as zeros
+    auto table8 = [&](const uint16_t* t, int st, int ng) {
+        u32x4 v;
+        __builtin_memcpy(&v, t + g0 + 8 * st, 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int left = ng - 8 * st - 2 * j;
+            v[j] &= left >= 2 ? 0xFFFFFFFFu : left == 1 ? 0xFFFFu : 0u;
+        }
+        return v;
+    };
+    u32x4 rv[CPW][2][BITS / 4];
+    auto load_weights = [&] {
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) ww.load(ch0 + i, rv[i]);
+    };
 
+    // A wave's loads return in order.  So first what is needed first: the tables,
+    // and gate|up's activations; down's have to wait for gate|up, and the wave that
+    // waits (all others have their weights in flight meanwhile) keeps its weights
+    // back.
+    const bool idle = u0 == u1;
+    int tile_now = idle ? -1 : tile_of(u0);
+    if (!idle) {
+        load_tables(0);
+        if constexpr (!kDown) load_x(tile_now);
+        aim(u0);
+        if (!kDown || wave != 0) load_weights();
+        store_tables(0);
+        if constexpr (!kDown) {
+            split_sums();
+            loads_done();
+        }
+    } else {
+        load_tables(0);
+        store_tables(0);
+    }
+    if constexpr (kDown) {
+        const int t = tile_of(lo) + lane;  // at most 6 tiles
+        if (wave == 0 && lo < hi && t * upt < hi)
+            if (!wait_for(a.done_gateup + t * kPad, a.I / 16)) give_up(a);
+        __syncthreads();
+        if (!idle) {
+            load_x(tile_now);
+            if (wave == 0) load_weights();
+            split_sums();
+            loads_done();
+        }
+    }
     const CodeConsts<OFF> kc = code_consts<OFF>(a.zero);
-    const int parts_row = 2 * K;  // values of a row's hi and lo parts
-    const Rsrc rx = make_rsrc(kDown ? a.h : a.n, 2u * parts_row * static_cast<uint32_t>(kDown ? a.T * a.k : a.T));
-    u32x4 x[kChunks][4];
-    int tile_now = -1;
     __syncthreads();
     for (int step = 0; step < steps; ++step) {
         const int u = u0 + step;
-        const bool busy = u < u1, more = u + 1 < u1;
-        if (step + 1 < steps) load_tables(step + 1);
-        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (busy) {
-            const int tile = __builtin_amdgcn_readfirstlane(u / upt);
+        load_tables(step + 1);
+        if (!idle) {
+            const int tile = tile_of(min(u, u1 - 1));
             if (tile != tile_now) {
                 tile_now = tile;
-                if constexpr (kDown) {
-                    if (!wait_for(a.done_gateup + tile, a.I / 16)) give_up(a);
+                load_x(tile);
+                split_sums();
+                loads_done();
+            }
+            aim(u + 1);
+            const uint16_t* const ts = sm.tables[step & 1][0] + (32 * wu + lr) * G;
+            const uint16_t* const tb = sm.tables[step & 1][1] + (32 * wu + lr) * G;
+            const int ngl = fresh(ng);
+            f32x4 acc[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int st = 0; st < NS; ++st) {
+                    acc[b] = mfma16(xb[st], table8(tb + 16 * b * G, st, ngl), acc[b]);
+                    if constexpr (OFF != 0) acc[b] = mfma16(xo[st], table8(ts + 16 * b * G, st, ngl), acc[b]);
                 }
-                // operand row lr: part lr / 8 of the tile's row lr % 8; rows past the
-                // tile and columns past K are zeros
-                const int count = sm.l.count[tile], r = lr & 7;
-                const int slot = sm.l.rows[tile][min(r, count - 1)];
-                const uint32_t base = 2u * (static_cast<uint32_t>(kDown ? slot : slot / a.k) * parts_row + (lr >> 3) * K);
+            }
+            constexpr int NB = kBuffers<BITS>;
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i)
+            for (int h = 0; h < CPW; h += NB) {
+                // the weights of this unit through LDS, those of the next into their place
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int col = 128 * (ch0 + i) +
-                                        (kChainCols<GS> == 64 ? 64 * (s >> 1) + 16 * q + 8 * (s & 1) : 32 * s + 8 * q);
-                        const uint32_t at = i < nc && r < count && col < K ? base + 2u * col : 0xFFFFFFF0u;
-                        x[i][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, at, 0, kDown ? kSc1 : 0));
+                for (int i = h; i < h + NB && i < CPW; ++i) {
+                    ww.lds = sm.w[wave][i - h];
+                    ww.put(rv[i]);
+                    ww.load(ch0 + i, rv[i]);
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = h; i < h + NB && i < CPW; ++i) {
+                    chunk_fence();  // one chunk's operands at a time: registers
+                    ww.lds = sm.w[wave][i - h];
+                    WLane<BITS> wv[2];
+                    float s[2][CH];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        wv[b] = ww.get(b, lr, q);
+#pragma unroll
+                        for (int j = 0; j < CH; ++j)
+                            s[b][j] = bf16_to_f32(ts[16 * b * G + min(g0 + ((i * CH + j) >> SH), G - 1)]);
                     }
-                // chain sums of the wave's slice
-#pragma unroll
-                for (int i = 0; i < kChunks * CH / 4; ++i) {
-                    const int p = lane + 64 * i, c = p >> 4, row = p & 15, rr = row & 7;
-                    const int chain = ch0 * CH + c;
-                    float sum = 0.f;
-                    if (c < nc * CH && chain < chains && rr < count) {
-                        const int sl = sm.l.rows[tile][rr];
-                        if constexpr (kDown) {
-                            const int blocks = kChainCols<GS> / 16;
-                            const Rsrc rs = make_rsrc(a.hsum, 8u * (K / 16) * static_cast<uint32_t>(a.T * a.k));
-                            const uint32_t at = 4u * ((2 * sl + (row >> 3)) * (K / 16) + chain * blocks);
-                            float v[kChainCols<GS> / 16];
-#pragma unroll
-                            for (int b = 0; b < blocks; ++b)
-                                v[b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at + 4 * b, 0, kSc1));
-#pragma unroll
-                            for (int b = 0; b < blocks; ++b) sum += v[b];
-                        } else {
-                            sum = a.nsum[static_cast<size_t>(2 * (sl / a.k) + (row >> 3)) * chains + chain];
-                        }
-                    }
-                    sm.xs[wave][c][row] = sum;
+                    // columns past the slice have zeros in x
+                    chunk_steps<GS, 2, 4, BITS>(acc, x[i], wv, s, kc);
                 }
                 __builtin_amdgcn_wave_barrier();
             }
-            if (more) aim(u + 1);
-            const uint16_t* const ts = sm.tables[step & 1] + wu * 64 * G + lr * G;
+            // operand rows 8..15 are the lo parts of rows 0..7, in the wave's upper half:
+            // the halves trade places so that the lower one adds up block 0, the upper
+            // one block 1
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                if (i < nc) {
-                    chunk_fence();
-                    ww.put(rv[i]);
-                    if (more) ww.load(ch0 + i, rv[i]);
-                    __builtin_amdgcn_wave_barrier();
-                    WLane<BITS> wv[2];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) wv[b] = ww.get(b, lr, q);
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        const f32x4 X = *reinterpret_cast<const f32x4*>(&sm.xs[wave][i * CH + j][4 * q]);
-                        const int g = min(((ch0 + i) * CH + j) >> SH, G - 1);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            f32x4 p;
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) p[v] = -static_cast<float>(OFF) * X[v];
-#pragma unroll
-                            for (int m = 0; m < MPG; ++m)
-                                p = mfma16(x[i][j * MPG + m], slice_operand<BITS, OFF>(wv[b], j * MPG + m, kc), p);
-                            const float s = bf16_to_f32(ts[16 * b * G + g]), bias = bf16_to_f32(ts[(32 + 16 * b) * G + g]);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) acc[b][v] = fmaf(bias, X[v], fmaf(s, p[v], acc[b][v]));
-                        }
-                    }
-                    __builtin_amdgcn_wave_barrier();
-                }
+            for (int v = 0; v < 4; ++v) {
+                const u32x2 t = __builtin_bit_cast(
+                    u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[0][v]), __float_as_uint(acc[1][v]), false, false));
+                sm.red[step & 1][wave][lane >> 5][4 * (q & 1) + v][lr] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
             }
-            // operand rows 8..15 are the lo parts of rows 0..7
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    acc[b][v] += __shfl_xor(acc[b][v], 32);
-                    if (lane < 32) sm.red[step & 1][wave][b][4 * q + v][lr] = acc[b][v];
-                }
         }
-        if (step + 1 < steps) store_tables(step + 1);
+        store_tables(step + 1);
         __syncthreads();
-        // the units' outputs: 128 of gate|up, 256 of down each
-        constexpr int kOut = kDown ? 256 : 128;
-        for (int p = tid; p < nu * kOut; p += kFewThreads) {
-            const int i = p / kOut, r = (p / (kOut / kTileRows)) % kTileRows, c = p % (kOut / kTileRows);
-            const int uu = first(range * nu + i) + step;
-            if (uu >= first(range * nu + i + 1)) continue;
-            const int tile = uu / upt, col = uu - tile * upt;
-            if (r >= sm.l.count[tile]) continue;
-            const size_t slot = sm.l.rows[tile][r];
+        // the units' outputs: wave r adds up the shares of row r, 16 columns of both
+        // halves of gate|up by 4 lanes each, 32 of down by 2
+        constexpr int kCols = kDown ? 32 : 16;
+        const int r = wave, c = lane % kCols;
+        for (int i = 0; i < nu; ++i) {
+            const int uu = first(r0 + i) + step;
+            if (uu >= first(r0 + i + 1)) continue;
+            const int t = tile_of(uu), col = uu - t * upt;
+            if (r >= uniform(sm.l.count[t])) continue;
+            const int id = uniform(sm.l.rows[t][r]);
+            const size_t slot = (id >> 6) * a.k + (id & 63);
             float o[2] = {0.f, 0.f};
-            for (int v = 0; v < split; ++v) {
+            for (int v = lane / kCols; v < split; v += 64 / kCols) {
                 const auto& red = sm.red[step & 1][(i << log_split) + v];
                 if constexpr (kDown) {
                     o[0] += red[c >> 4][r][c & 15];
@@ -460,33 +601,52 @@ __device__ __forceinline__ void run_range(const LayerArgs& a, FewSmem<GS, BITS>&
                     o[1] += red[1][r][c];
                 }
             }
+#pragma unroll
+            for (int off = kCols; off < 64; off <<= 1) {
+                o[0] += __shfl_xor(o[0], off);
+                if constexpr (!kDown) o[1] += __shfl_xor(o[1], off);
+            }
             if constexpr (kDown) {
                 const Rsrc ry = make_rsrc(a.y + slot * a.H, 4u * a.H);
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[0]), ry, 4 * (32 * col + c), 0, kSc1);
+                if (lane < kCols)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[0]), ry, 4 * (32 * col + c), 0, kSc1);
             } else {
                 const float hv = (a.swiglu ? silu(o[0]) : gelu_tanh(o[0])) * o[1];
                 const uint16_t hi16 = f32_to_bf16(hv), lo16 = f32_to_bf16(hv - bf16_to_f32(hi16));
-                const Rsrc rh = make_rsrc(a.h, 4u * a.I * static_cast<uint32_t>(a.T * a.k));
-                const uint32_t at = 2u * (static_cast<uint32_t>(slot) * 2 * a.I + 16 * col + (c & 8) + permuted_pos(c & 7));
-                __builtin_amdgcn_raw_buffer_store_b16(hi16, rh, at, 0, kSc1);
-                __builtin_amdgcn_raw_buffer_store_b16(lo16, rh, at + 2u * a.I, 0, kSc1);
                 const float shi = sum16(bf16_to_f32(hi16)), slo = sum16(bf16_to_f32(lo16));
-                const Rsrc rs = make_rsrc(a.hsum, 8u * (a.I / 16) * static_cast<uint32_t>(a.T * a.k));
-                const uint32_t sat = 4u * (static_cast<uint32_t>(slot) * 2 * (a.I / 16) + col);
-                if (c < 2)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(c ? slo : shi), rs, sat + (c ? 4u * (a.I / 16) : 0), 0,
+                // lanes 0..15 store the hi parts, 16..31 the lo parts
+                const Rsrc rh = make_rsrc(a.h, 4u * a.I * static_cast<uint32_t>(a.T * a.k));
+                const uint32_t part = 2 * static_cast<uint32_t>(slot) + (lane >> 4);
+                if (lane < 32)
+                    __builtin_amdgcn_raw_buffer_store_b16(lane < 16 ? hi16 : lo16, rh,
+                                                          2u * (part * a.I + 16 * col + (c & 8) + permuted_pos(c & 7)), 0, kSc1);
+                const Rsrc rq = make_rsrc(a.hsum, 8u * (a.I / 16) * static_cast<uint32_t>(a.T * a.k));
+                if (lane == 0 || lane == 16)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lane ? slo : shi), rq, 4u * (part * (a.I / 16) + col), 0,
                                                           kSc1);
             }
         }
     }
-    // the range is done once its stores have been acknowledged
+    // the range is done once its stores have been acknowledged; the phase's flags
+    // are read meanwhile
+    const int taken = tid < kRanges ? __hip_atomic_load(flags + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    const int t0 = lo / upt + tid;
-    if (t0 * upt < hi) {
+    const bool left = __syncthreads_or(!taken);
+    const int t0 = tile_of(lo) + tid;
+    if (lo < hi && t0 * upt < hi) {
         const int n = min(hi, (t0 + 1) * upt) - max(lo, t0 * upt);
-        __hip_atomic_fetch_add((kDown ? a.done_down : a.done_gateup) + t0, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_fetch_add((kDown ? a.done_down : a.done_gateup) + t0 * kPad, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    return left;
+}
+
+// The same with the chunks of a wave's slice known: 3, or 4.
+template <int GS, int BITS, bool kDown>
+__device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>& sm, int range, const int32_t* flags) {
+    const int nch = ((kDown ? a.I : a.H) + 127) / 128;
+    const int log_split = split_log(nch), most = (nch + (1 << log_split) - 1) >> log_split;
+    return most <= 3 ? run_range<GS, BITS, kDown, 3>(a, sm, range, flags)
+                     : run_range<GS, BITS, kDown, 4>(a, sm, range, flags);
 }
 
 // out and normed of one token.
@@ -496,10 +656,10 @@ __device__ __forceinline__ void finish_token(const LayerArgs& a, FewSmem<GS, BIT
     norm::Row<kWaves, 1, 8, -1> row;
     row.load(a.tail, t, c0);
     if (static_cast<int>(threadIdx.x) < k)  // lanes of the first wave
-        if (!wait_for(a.done_down + sm.l.slot_tile[t * k + threadIdx.x], H / 32)) give_up(a);
+        if (!wait_for(a.done_down + sm.l.slot_tile[t * k + threadIdx.x] * kPad, H / 32)) give_up(a);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    const bool ok = !__hip_atomic_load(a.failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int failed = __hip_atomic_load(a.failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     float z[1][8] = {};
     const Rsrc ry = make_rsrc(a.y + static_cast<size_t>(t) * k * H, 4u * H * k);
     for (int j0 = 0; j0 < k; j0 += 8) {
@@ -521,7 +681,7 @@ __device__ __forceinline__ void finish_token(const LayerArgs& a, FewSmem<GS, BIT
             }
         }
     }
-    if (!ok) {
+    if (failed) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[0][i] = __uint_as_float(0x7FC00000u);
     }
@@ -532,12 +692,12 @@ template <int GS, int BITS>
 __global__ __launch_bounds__(kFewThreads, 1) void moe_layer_few_experts(LayerArgs a) {
     __shared__ FewSmem<GS, BITS> sm;
     make_lists(a, sm);
-    for (int r = take(sm, a.claim_gateup, kRanges, blockIdx.x); r >= 0; r = take(sm, a.claim_gateup, kRanges, -1))
-        run_range<GS, BITS, false>(a, sm, r);
-    for (int r = take(sm, a.claim_down, kRanges, blockIdx.x); r >= 0; r = take(sm, a.claim_down, kRanges, -1))
-        run_range<GS, BITS, true>(a, sm, r);
-    for (int t = take(sm, a.claim_token, a.T, blockIdx.x % a.T); t >= 0; t = take(sm, a.claim_token, a.T, -1))
-        finish_token(a, sm, t);
+    // usually one range of each phase; more if workgroups have not started yet
+    for (int r = sm.own[0] ? blockIdx.x : take(sm, a.claim_gateup, kRanges); r >= 0;)
+        r = run_range<GS, BITS, false>(a, sm, r, a.claim_gateup) ? take(sm, a.claim_gateup, kRanges) : -1;
+    for (int r = sm.own[1] ? blockIdx.x : take(sm, a.claim_down, kRanges); r >= 0;)
+        r = run_range<GS, BITS, true>(a, sm, r, a.claim_down) ? take(sm, a.claim_down, kRanges) : -1;
+    if (static_cast<int>(blockIdx.x) < a.T) finish_token(a, sm, blockIdx.x);
 }
 
 template <int GS, int BITS>

@@ -313,12 +313,14 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
 
 // The layer for few tokens (layer_few.hip).
 constexpr int kLayerFewTokens = 16;
+constexpr int kLayerCounterStride = 32;
 constexpr int kLayerRanges = 256;  // shares of each matmul phase: one workgroup a CU
 struct LayerArgs {
     int32_t T, k, E, H, I, gs, bits;
     bool swiglu, norm, norm_f32;
     float eps, weight_offset;
     uint32_t zero;  // always 0 (see CodeConsts)
+    uint32_t magic_gateup, magic_down;  // 2^32 / units of a tile, rounded up
     RouterArgs router;
     const float* expert_scale;
     const uint16_t* x;
@@ -331,12 +333,12 @@ struct LayerArgs {
     // workspace
     int32_t* counters;   // the arrays below, cleared by the first launch
     int32_t num_counters;
-    int32_t *claim_gateup, *claim_down, *claim_token;  // [kLayerRanges], [kLayerRanges], [kLayerFewTokens]
-    int32_t *done_gateup, *done_down;                  // units done per tile: [T * k] each
+    int32_t *claim_gateup, *claim_down;                // [kLayerRanges] each: range taken
+    int32_t *done_gateup, *done_down;                  // units done per tile: [T * k] each, kLayerCounterStride apart
     int32_t* failed;                                   // [1]: a bounded wait ran out
     float* logits;       // [T, E]
     uint16_t* n;         // [T, 2, H]: rms(x) as bf16 hi and lo, pieces permuted
-    float* nsum;         // [T, 2, H / chain]: their sums over chains of 64 (group size 32: 32) columns
+    float* nsum;         // [T, 2, H / gs]: their sums over groups
     uint16_t* h;         // [T * k, 2, I]
     float* hsum;         // [T * k, 2, I / 16]: sums over 16 columns
     float* y;            // [T * k, H]
