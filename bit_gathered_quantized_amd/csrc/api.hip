@@ -422,8 +422,10 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
         a.norm_f32 = l->norm_type == MOE_T_FP32;
         a.eps = l->eps;
         a.weight_offset = l->weight_offset;
-        a.magic_gateup = static_cast<uint32_t>(((1ull << 32) + p->I / 16 - 1) / (p->I / 16));
-        a.magic_down = static_cast<uint32_t>(((1ull << 32) + p->H / 32 - 1) / (p->H / 32));
+        const uint32_t upt_gateup = p->I / 16;
+        const uint32_t upt_down = p->H / 32;
+        a.magic_gateup = ((1u << 31) + upt_gateup - 1) / upt_gateup;
+        a.magic_down = ((1u << 31) + upt_down - 1) / upt_down;
         a.router = router_args(&r, x, logits);
         a.expert_scale = l->expert_scale;
         a.x = static_cast<const uint16_t*>(x);

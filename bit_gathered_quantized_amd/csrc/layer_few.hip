@@ -11,7 +11,11 @@
 // The time is that of reading each touched expert's weights once.  So the second
 // launch holds the chip from the first byte to the last: one workgroup of eight
 // waves a CU, whose waves have the weights of their next 32 rows in flight while
-// they multiply the present ones, through the whole list of experts.
+// they multiply the present ones, through the whole list of experts.  128 experts
+// top-8, hidden 2816, expert width 704, one launch after the other: 8 tokens of
+// 4-bit codes 66 us (174 MB), of which the weights stream for 40 us at 4.5 TB/s and
+// 7 us are the first launch, 5 the lists, 4 the first loads, 4 the turn from gate|up
+// to down, 5 the tokens; one token 31 us, 16 tokens of 8-bit codes 135 us (550 MB).
 //
 // Tiles.  An expert's rows go in tiles of at most 8: a 16-row MFMA operand holds
 // the hi parts of 8 rows and their lo parts below, so 16-bit activations cost no
@@ -23,19 +27,28 @@
 // parts in three of the four 8-value pieces of K, exact to its last bit.
 //
 // A unit is 32 weight rows (gate|up: 16 columns of h, both halves; down: 32
-// output columns) by all of K, cut over SPLIT waves that hold at most 4 chunks of
-// 128 columns each, so that a wave keeps its slice of the tile's activations in
-// registers for all units of the tile.  Units are numbered tile by tile, and
-// workgroup b takes the b-th of 256 equal ranges of them.
+// output columns) by all of K, cut over 1, 2, 4 or 8 waves that hold at most 4
+// chunks of 128 columns each, so that a wave keeps its slice of the tile's
+// activations in registers for all units of the tile.  Few waves to a unit and long
+// slices: a unit costs a wave 2 us whatever it holds, so 3 chunks instead of 2 in the
+// down matmul above (2 waves, not 4) took it from 18 to 11 us.  Units are numbered
+// tile by tile, and workgroup b takes the b-th of 256 equal ranges of them.
+//
+// Nothing in a range makes its waves wait for one another but the places for their
+// shares of a unit, and those are four deep; a barrier a unit cost 8 tokens 8 us, and
+// outputs made by whoever came last (the slowest wave, ever later) 8 us as well.
+// Scales and biases are loaded by the wave that needs them, through its own LDS.
 //
 // Order between the phases without a barrier.  A range is taken by an exchange on
 // its own flag.  A workgroup takes its own range of both matmuls when it starts,
-// then, at the end of a phase, any range of it that is still untaken, and only
-// when all ranges of a phase are taken does it wait for the counters (units done
-// per tile) of that phase; workgroup t finishes token t at last.  So whoever waits waits for running workgroups, for
-// ranges of an earlier phase than its own, and the first phase waits for nobody:
-// every wait ends, however few workgroups the GPU holds at once.  (Waits are also bounded: a workspace that another call writes to gives
-// NaN, not a hang.)
+// then, at the end of a phase, any range of it that is still untaken, and only when
+// all ranges of a phase are taken does it go on: in the down matmul it waits for the
+// counters (gate|up units done) of its range's tiles, and workgroup t, which makes
+// token t's output at last, for those of the token's tiles.  So whoever waits waits
+// for running workgroups, for ranges of an earlier phase than its own, and the first
+// phase waits for nobody: every wait ends, however few workgroups the GPU holds at
+// once.  (Waits are also bounded: a workspace that another call writes to gives NaN,
+// not a hang.)
 //
 // What one workgroup writes and another reads within the launch (h and its sums,
 // y) is stored and loaded past the L2 of the XCD (sc1), rows of whole 128-byte
@@ -54,7 +67,6 @@ constexpr int kWaves = 8, kFewThreads = 64 * kWaves;
 constexpr int kRanges = kLayerRanges;
 constexpr int kTileRows = 8;
 constexpr int kMaxSlots = kLayerFewTokens * kRouterMaxK;  // assignments, and so tiles
-constexpr int kChunks = 4;                                // chunks of 128 columns a wave holds
 constexpr int kSc1 = 16;                                  // buffer access past the XCD's L2
 constexpr int kPad = kLayerCounterStride;                 // counters lie on cache lines of their own
 constexpr int kSpinLimit = 1 << 22;                       // polls of about 1 us
@@ -135,46 +147,56 @@ __global__ __launch_bounds__(256) void moe_layer_few_route(LayerArgs a) {
 }
 
 // ----------------------------------------------------------- second launch
-// The lists that every workgroup makes of the chosen experts.
+// The lists that every workgroup makes of the chosen experts.  The assignments lie
+// in h, its sums and y in the order of the tiles: row `start` + r is row r of a tile.
 struct Lists {
-    int32_t tiles;                             // tiles in all
-    uint16_t rows[kMaxSlots][kTileRows];       // 64 t + j of a tile's rows
-    uint16_t expert[kMaxSlots];                // a tile's expert
-    uint8_t count[kMaxSlots];                  // and its rows
-    uint16_t slot_tile[kMaxSlots];             // the tile of an assignment
-    float weight[kMaxSlots];                   // its routing weight
+    int32_t tiles;                    // tiles in all
+    uint32_t tokens[kMaxSlots];       // the tokens of a tile's rows, 4 bits each
+    uint16_t what[kMaxSlots];         // 16 * its expert + its rows
+    uint16_t start[kMaxSlots];        // its first row
+    uint16_t slot_tile[kMaxSlots];    // the tile of assignment t * k + j
+    uint16_t slot_row[kMaxSlots];     // and its row in h and y
+    float weight[kMaxSlots];          // and its routing weight
 };
 
-// Chunks that a wave turns at a time: all of a unit with 4-bit codes, half of it
-// with 8-bit ones (LDS).
+// Buffers in which a wave turns its weights: a unit's chunks at once where there is room.
 template <int BITS>
-constexpr int kBuffers = BITS == 4 ? kChunks : kChunks / 2;
+constexpr int kBuffers = BITS == 4 ? 4 : 2;
 
-// 16-byte pieces of scales (or biases) of the units at work per thread of half a
-// workgroup: units times columns are at most 4096.
+// The table row of a wave's slice (at most 512 columns): pieces of 16 bytes, from the
+// piece in which the slice begins on.
 template <int GS>
-constexpr int kTablePieces = 4 * 4096 / GS / (kFewThreads / 2) > 0 ? 4 * 4096 / GS / (kFewThreads / 2) : 1;
+constexpr int kTablePieces = 512 / GS <= 8 ? 2 : 4;
 
-// A row of nch chunks is cut over 1 << split_log waves.
-__device__ __forceinline__ int split_log(int nch) { return nch <= 4 ? 0 : nch <= 8 ? 1 : nch <= 16 ? 2 : 3; }
+// Places for the shares of a unit's waves, and units after which its outputs are made.
+constexpr int kDepth = 4, kLag = 2;
+
+// A row of nch chunks is cut over 1 << split_log waves, 4 chunks to a wave at most.
+__device__ __forceinline__ int split_log(int nch) { return nch <= 3 ? 0 : nch <= 6 ? 1 : nch <= 12 ? 2 : 3; }
 
 template <int GS, int BITS>
 struct alignas(16) FewSmem {
-    uint32_t w[kWaves][kBuffers<BITS>][2 * 16 * 4 * BITS];  // weight transposition, a wave's own
-    uint16_t tables[2][2][kTablePieces<GS> * kFewThreads / 2 * 8];  // scales, biases of the units at work, of the next ones
-    float red[2][kWaves][2][kTileRows][16];         // the waves' shares of the units' outputs
+    uint32_t w[kWaves][kBuffers<BITS>][2 * 16 * 4 * BITS];   // weight transposition, a wave's own
+    u32x4 tables[kWaves][2][2][16][kTablePieces<GS>];        // scales, biases of its slice of a unit
+    float red[kDepth][kWaves][2][kTileRows][16];             // the waves' shares of the units' outputs
+    int32_t arrived[kDepth][kWaves], finished[kDepth][kWaves];
     union {
-        struct {
-            uint32_t mask[MOE_MAX_EXPERTS];     // tokens of each expert
-            uint16_t base[MOE_MAX_EXPERTS];     // its first tile
+        struct {                             // while the lists are made
+            uint32_t mask[MOE_MAX_EXPERTS];  // tokens of each expert
+            uint16_t tile[MOE_MAX_EXPERTS];  // its first tile
+            uint16_t row[MOE_MAX_EXPERTS];   // and row
             uint16_t id[kMaxSlots];
             uint32_t scan[kWaves];
         };
-        float lds[2][16];                       // sums of the last phase
+        float lds[2][16];                    // sums of the last phase
     };
     int32_t pick, own[2];
     Lists l;
 };
+
+// A value that is the same in every lane, as a scalar (one read from LDS is not
+// known to be).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // One relaxed device-wide read of *p, polled until it reaches `want`.
 __device__ __forceinline__ bool wait_for(const int32_t* p, int32_t want) {
@@ -187,21 +209,32 @@ __device__ __forceinline__ bool wait_for(const int32_t* p, int32_t want) {
     return ok;
 }
 
+// The same in LDS, for another wave of the workgroup.
+__device__ __forceinline__ bool wait_lds(const int32_t* p, int32_t want) {
+    bool ok = false;
+    for (int i = 0; i < kSpinLimit && !ok; ++i) {
+        ok = uniform(__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) >= want;
+        if (!ok) __builtin_amdgcn_s_sleep(1);
+    }
+    asm volatile("" ::: "memory");
+    return ok;
+}
+
 // A wait ran out: every token becomes NaN.
 __device__ __forceinline__ void give_up(const LayerArgs& a) {
     __hip_atomic_store(a.failed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Takes any untaken one of n <= kFewThreads flags; -1 once all are taken.  Called
-// by the whole workgroup.
+// Takes any untaken range of a phase; -1 once all are taken.  Called by the whole
+// workgroup.
 template <class Smem>
-__device__ __forceinline__ int take(Smem& sm, int32_t* flags, int n) {
+__device__ __forceinline__ int take(Smem& sm, int32_t* flags) {
     for (;;) {
         __syncthreads();
         if (threadIdx.x == 0) sm.pick = INT32_MAX;
         __syncthreads();
-        const int i = threadIdx.x;
-        if (i < n && !__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMin(&sm.pick, i);
+        for (int i = threadIdx.x; i < kRanges; i += kFewThreads)
+            if (!__hip_atomic_load(flags + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMin(&sm.pick, i);
         __syncthreads();
         const int want = sm.pick;
         if (want == INT32_MAX) return -1;
@@ -218,64 +251,98 @@ template <class Smem>
 __device__ __forceinline__ void make_lists(const LayerArgs& a, Smem& sm) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int T = a.T, k = a.k, E = a.E;
-    // the last wave (the first ones have a token each) takes the workgroup's ranges
+    // the last wave (the first ones have most tokens) takes the workgroup's ranges
     if (wave == kWaves - 1 && lane < 2)
         sm.own[lane] = !__hip_atomic_exchange((lane ? a.claim_down : a.claim_gateup) + blockIdx.x, 1, __ATOMIC_RELAXED,
                                               __HIP_MEMORY_SCOPE_AGENT);
     for (int e = threadIdx.x; e < E; e += kFewThreads) sm.mask[e] = 0;
-    for (int t = wave; t < T; t += kWaves) {
-        const float* row = a.logits + static_cast<size_t>(t) * E;
-        TopK c;
-        if (E <= 128) {
-            float v[2];
+    // tokens wave, wave + 8; the factors of the weights, and they, are needed at last
+    TopK c[kLayerFewTokens / kWaves];
+    float factor[kLayerFewTokens / kWaves], first[kLayerFewTokens / kWaves][2];
+    const Rsrc logits = make_rsrc(a.logits, 4u * T * E);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) v[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
-            c = wave_topk<2>(v, E, k, a.expert_scale);
+    for (int i = 0; i < kLayerFewTokens / kWaves; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+            first[i][n] = __uint_as_float(
+                __builtin_amdgcn_raw_buffer_load_b32(logits, 4u * ((wave + kWaves * i) * E + lane + 64 * n), 0, 0));
+#pragma unroll
+    for (int i = 0; i < kLayerFewTokens / kWaves; ++i) {
+        const int t = wave + kWaves * i;
+        if (t >= T) break;
+        const float* row = a.logits + static_cast<size_t>(t) * E;
+        if (E <= 128 && k <= 16) {
+            c[i] = wave_topk_128(first[i][0], first[i][1], E, k);
         } else {
             float v[MOE_MAX_EXPERTS / 64];
 #pragma unroll
-            for (int i = 0; i < MOE_MAX_EXPERTS / 64; ++i) v[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
-            c = wave_topk<MOE_MAX_EXPERTS / 64>(v, E, k, a.expert_scale);
+            for (int n = 0; n < MOE_MAX_EXPERTS / 64; ++n) v[n] = lane + 64 * n < E ? row[lane + 64 * n] : -INFINITY;
+            c[i] = wave_topk<MOE_MAX_EXPERTS / 64>(v, E, k, nullptr);
         }
-        if (lane < k) {
-            sm.id[t * k + lane] = static_cast<uint16_t>(c.id);
-            sm.l.weight[t * k + lane] = c.weight;
-            if (blockIdx.x == 0 && a.out_ids) a.out_ids[t * k + lane] = c.id;
-            if (blockIdx.x == 0 && a.out_weights) a.out_weights[t * k + lane] = c.weight;
-        }
+        if (lane < k) sm.id[t * k + lane] = static_cast<uint16_t>(c[i].id);
+        factor[i] = a.expert_scale && lane < k ? a.expert_scale[c[i].id] : 1.f;
     }
     __syncthreads();
     for (int s = threadIdx.x; s < T * k; s += kFewThreads) atomicOr(&sm.mask[sm.id[s]], 1u << (s / k));
     __syncthreads();
-    // tiles before expert 2 i, by thread i (E <= 1024 = 2 kFewThreads)
-    const int e0 = 2 * threadIdx.x;
-    auto tiles_of = [&](int e) { return e < E ? (__popc(sm.mask[e]) + kTileRows - 1) / kTileRows : 0; };
-    const int n0 = tiles_of(e0), n1 = tiles_of(e0 + 1);
-    int incl = n0 + n1;
+    // tiles and rows before expert kPer i, by thread i: rows << 16 | tiles
+    constexpr int kPer = MOE_MAX_EXPERTS / kFewThreads;
+    const int e0 = kPer * threadIdx.x;
+    uint32_t of[kPer], incl = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t rows = e0 + i < E ? __popc(sm.mask[e0 + i]) : 0;
+        of[i] = rows << 16 | (rows + kTileRows - 1) / kTileRows;
+        incl += of[i];
+    }
+    const uint32_t own = incl;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(incl, off);
+        const uint32_t o = __shfl_up(incl, off);
         if (lane >= off) incl += o;
     }
     if (lane == 63) sm.scan[wave] = incl;
     __syncthreads();
-    int before = incl - n0 - n1;
+    uint32_t before = incl - own;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) before += w < wave ? sm.scan[w] : 0;
-    if (e0 < E) sm.base[e0] = static_cast<uint16_t>(before);
-    if (e0 + 1 < E) sm.base[e0 + 1] = static_cast<uint16_t>(before + n0);
-    if (threadIdx.x == kFewThreads - 1) sm.l.tiles = before + n0 + n1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (e0 + i < E) {
+            sm.tile[e0 + i] = static_cast<uint16_t>(before);
+            sm.row[e0 + i] = static_cast<uint16_t>(before >> 16);
+        }
+        before += of[i];
+    }
+    if (threadIdx.x == kFewThreads - 1) sm.l.tiles = before & 0xFFFF;
     __syncthreads();
     for (int s = threadIdx.x; s < T * k; s += kFewThreads) {
         const int e = sm.id[s], t = s / k;
-        const uint32_t m = sm.mask[e];
-        const int rank = __popc(m & ((1u << t) - 1u)), tile = sm.base[e] + rank / kTileRows;
-        sm.l.rows[tile][rank % kTileRows] = static_cast<uint16_t>(64 * t + s - t * k);
+        uint32_t m = sm.mask[e];
+        const int rank = __popc(m & ((1u << t) - 1u)), rows = __popc(m), tile = sm.tile[e] + rank / kTileRows;
         sm.l.slot_tile[s] = static_cast<uint16_t>(tile);
-        if (rank % kTileRows == 0) {
-            sm.l.expert[tile] = static_cast<uint16_t>(e);
-            sm.l.count[tile] = static_cast<uint8_t>(min(kTileRows, __popc(m) - rank));
+        sm.l.slot_row[s] = static_cast<uint16_t>(sm.row[e] + rank);
+        if (rank % kTileRows == 0) {  // the tile's first row writes the tile
+            const int count = min(kTileRows, rows - rank);
+            m >>= t;
+            uint32_t tokens = 0;
+            for (int r = 0; r < count; ++r) {
+                tokens |= static_cast<uint32_t>(t + __ffs(m) - 1) << (4 * r);
+                m &= m - 1;
+            }
+            sm.l.tokens[tile] = tokens;
+            sm.l.what[tile] = static_cast<uint16_t>(16 * e + count);
+            sm.l.start[tile] = static_cast<uint16_t>(sm.row[e] + rank);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kLayerFewTokens / kWaves; ++i) {
+        const int s = (wave + kWaves * i) * k + lane;
+        if (wave + kWaves * i >= T || lane >= k) break;
+        const float w = c[i].weight * factor[i];
+        sm.l.weight[s] = w;
+        if (blockIdx.x == 0 && a.out_ids) a.out_ids[s] = c[i].id;
+        if (blockIdx.x == 0 && a.out_weights) a.out_weights[s] = w;
     }
     __syncthreads();
 }
@@ -307,10 +374,6 @@ __device__ __forceinline__ void load_sums(float (&v)[8], Rsrc all, uint32_t at, 
         }
     }
 }
-
-// A value that is the same in every lane, as a scalar (one read from LDS is not
-// known to be).
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // v as a value that the compiler forms anew here: what follows from it is computed
 // where it is used, not kept in registers through the loop.
@@ -352,61 +415,48 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     auto first = [&](int share) { return N * share >> shift; };
     const int r0 = range * nu, lo = first(r0), hi = first(r0 + nu);
     const int u0 = first(r0 + wu), u1 = first(r0 + wu + 1);
-    // the shares of a range differ by one unit at most
-    int steps = 0;
-    for (int i = 0; i < nu; ++i) steps = max(steps, first(r0 + i + 1) - first(r0 + i));
-
-    // u / upt for u < 2^18, upt <= 256: u (m upt - 2^32) < 2^26 errs by less than 1 / upt
+    // u / upt for u < 2^18, upt <= 256, by m = ceil(2^31 / upt): u (m upt - 2^31) < 2^26,
+    // so the quotient errs by less than 1 / upt
     const uint32_t magic = kDown ? a.magic_down : a.magic_gateup;
-    auto tile_of = [&](int u) { return static_cast<int>(__umulhi(static_cast<uint32_t>(u), magic)); };
-    // the first weight row of block b of unit u
-    auto row_of = [&](int u, int b) {
-        const int tile = tile_of(u), i = u - tile * upt;
-        const uint32_t e = sm.l.expert[tile];
-        return e * rows_e + (kDown ? 32 * i + 16 * b : 16 * i + (b ? a.I : 0));
-    };
+    auto tile_of = [&](int u) { return static_cast<int>(__umulhi(2u * u, magic)); };
+    const int block_rows = kDown ? 16 : a.I;  // from its first block of 16 rows to its second
+    const int g0 = ch0 * 128 / GS, ng = min(nc * 128 / GS, G - g0);  // the slice's groups
+    const int cols = min(nc * 128, K - 128 * ch0);                   // and columns
+    // The tables' rows of a slice: lane (block, row, piece) loads pieces of 16 bytes.
+    // Where the slice begins in its first piece is the same for all units (16 rows are
+    // a multiple of 16 bytes).
+    const int tb_ = lane >> 5, tr_ = lane >> 1 & 15, tp_ = lane & 1;
+    const uint32_t tat = (2u * (tr_ * G + g0) & ~15u) + 2u * G * block_rows * tb_ + 16 * tp_;
     WaveW<2, GS, BITS> ww;
-    // ww loads unit u from now on, or nothing from u1 on
+    Rsrc rts, rtb;
+    // loads are of unit u from now on, or of nothing from u1 on
+    int ahead = 0;  // what[] of the unit to load next
+    auto look = [&](int u) { ahead = sm.l.what[tile_of(min(u, u1 - 1))]; };
     auto aim = [&](int u) {
-        const uint32_t* const w = kDown ? a.w_d : a.w_gu;
-        const uint32_t* blk[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const uint32_t r = uniform(row_of(min(u, u1 - 1), b));
-            blk[b] = w + static_cast<size_t>(r) * row_words;
-        }
+        const bool some = u < u1;
+        // its first weight row
+        const uint32_t r = uniform(ahead >> 4) * rows_e + (kDown ? 32 : 16) * (u - tile_of(u) * upt);
+        const uint32_t* const w = (kDown ? a.w_d : a.w_gu) + static_cast<size_t>(r) * row_words;
+        const uint32_t* const blk[2] = {w, w + static_cast<size_t>(block_rows) * row_words};
         ww.init(sm.w[wave][0], blk, row_words);
-        if (u >= u1) ww.blk[0] = ww.blk[1] = make_rsrc(w, 0);
+        const uint32_t left = 2u * G * (static_cast<uint32_t>(a.E) * rows_e - r);
+        rts = make_rsrc((kDown ? a.s_d : a.s_gu) + static_cast<size_t>(r) * G, some ? left : 0);
+        rtb = make_rsrc((kDown ? a.b_d : a.b_gu) + static_cast<size_t>(r) * G, some ? left : 0);
+        if (!some) ww.blk[0] = ww.blk[1] = make_rsrc(w, 0);
     };
-    // Tables: the scales of the units at work, then their biases, 2 G pieces of 16
-    // bytes a block of 16 rows.  The first half of the workgroup loads scales, the
-    // other biases, NP pieces a thread.
-    constexpr int kHalf = kFewThreads / 2;
-    const bool biases = wave >= kWaves / 2;
-    const uint16_t* const tab = kDown ? (biases ? a.b_d : a.s_d) : (biases ? a.b_gu : a.s_gu);
-    const Rsrc rt = make_rsrc(tab, 2u * a.E * rows_e * G);
-    int tu[NP];        // a piece's unit, its block and its place in the block
-    uint32_t tblk[NP], tat[NP];
+    u32x4 tv[2][NP / 2];
+    auto load_tables = [&] {
 #pragma unroll
-    for (int h = 0; h < NP; ++h) {
-        const int p = (tid & (kHalf - 1)) + kHalf * h, i = p / (4 * G), r = p - i * 4 * G;
-        tu[h] = i;
-        tblk[h] = r / (2 * G);
-        tat[h] = 16 * (r - tblk[h] * 2 * G);
-    }
-    u32x4 tv[NP];
-    auto load_tables = [&](int step) {
-#pragma unroll
-        for (int h = 0; h < NP; ++h) {
-            const int u = first(r0 + tu[h]) + step, end = first(r0 + tu[h] + 1);
-            const uint32_t at = 2u * G * row_of(max(min(u, end - 1), 0), tblk[h]) + tat[h];
-            tv[h] = load16(rt, tu[h] < nu && u < end ? at : 0xFFFFFFF0u, 0);
+        for (int i = 0; i < NP / 2; ++i) {
+            tv[0][i] = load16(rts, tat, 32 * i);
+            tv[1][i] = load16(rtb, tat, 32 * i);
         }
     };
-    auto store_tables = [&](int step) {
+    auto store_tables = [&] {
 #pragma unroll
-        for (int h = 0; h < NP; ++h)
-            *reinterpret_cast<u32x4*>(sm.tables[step & 1][biases] + 8 * ((tid & (kHalf - 1)) + kHalf * h)) = tv[h];
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < NP / 2; ++i) sm.tables[wave][t][tb_][tr_][2 * i + tp_] = tv[t][i];
     };
 
     // a tile's activations for this wave's slice: operand row lr is part lr / 8 of
@@ -415,15 +465,13 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     const Rsrc rx = make_rsrc(kDown ? a.h : a.n, 4u * K * slots);
     const Rsrc rs = kDown ? make_rsrc(a.hsum, 8u * (K / 16) * slots) : make_rsrc(a.nsum, 8u * G * slots);
     const Rsrc none = make_rsrc(a.n, 0);
-    u32x4 x[CPW][4], xb[NS], xo[NS];
+    u32x4 x[CPW][4], xb[NS];
     float sums[NS][8];
-    const int g0 = ch0 * 128 / GS, ng = min(nc * 128 / GS, G - g0);  // the slice's groups
-    const int cols = min(nc * 128, K - 128 * ch0);                   // and columns
     auto load_x = [&](int tile) {
         const int ng_ = fresh(ng), cols_ = fresh(cols);
-        const int count = sm.l.count[tile], r = lr & 7;
-        const int slot = sm.l.rows[tile][min(r, count - 1)];
-        const uint32_t src = 2u * static_cast<uint32_t>(kDown ? (slot >> 6) * a.k + (slot & 63) : slot >> 6) + (lr >> 3);
+        const int count = uniform(sm.l.what[tile]) & 15, r = lr & 7;
+        const uint32_t from = kDown ? sm.l.start[tile] + r : sm.l.tokens[tile] >> (4 * r) & 15;
+        const uint32_t src = 2u * from + (lr >> 3);
         // rows past the tile lie past every resource
         const bool mine = r < count;
         constexpr int B = kDown ? GS / 16 : 1;
@@ -448,7 +496,6 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
 #pragma unroll
         for (int st = 0; st < NS; ++st) {
             xb[st] = u32x4{0, 0, 0, 0};
-            xo[st] = xb[st];
 #pragma unroll
             for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -457,16 +504,15 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
                     const float p0 = __uint_as_float(pk << 16), p1 = __uint_as_float(pk & 0xFFFF0000u);
                     sums[st][2 * j] -= p0;
                     sums[st][2 * j + 1] -= p1;
-                    const uint32_t off = pack_bf16x2(-static_cast<float>(OFF) * p0, -static_cast<float>(OFF) * p1);
                     xb[st][j] = q == part ? pk : xb[st][j];
-                    xo[st][j] = q == part ? off : xo[st][j];
                 }
         }
     };
-    // eight entries of a table row, those past the slice as zeros
-    auto table8 = [&](const uint16_t* t, int st, int ng) {
+    // eight entries of a table row of the slice, those past the slice as zeros
+    const int tsub = 2 * (lr * G + g0) & 15;
+    auto table8 = [&](int t, int b, int st, int ng) {
         u32x4 v;
-        __builtin_memcpy(&v, t + g0 + 8 * st, 16);
+        __builtin_memcpy(&v, reinterpret_cast<const char*>(sm.tables[wave][t][b][lr]) + tsub + 16 * st, 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int left = ng - 8 * st - 2 * j;
@@ -475,9 +521,11 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
         return v;
     };
     u32x4 rv[CPW][2][BITS / 4];
+    // chunk i of the slice, or one past every row if the slice is shorter
+    auto chunk = [&](int i) { return i < nc ? ch0 + i : 1 << 20; };
     auto load_weights = [&] {
 #pragma unroll
-        for (int i = 0; i < CPW; ++i) ww.load(ch0 + i, rv[i]);
+        for (int i = 0; i < CPW; ++i) ww.load(chunk(i), rv[i]);
     };
 
     // A wave's loads return in order.  So first what is needed first: the tables,
@@ -486,22 +534,18 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     // back.
     const bool idle = u0 == u1;
     int tile_now = idle ? -1 : tile_of(u0);
+    if (tid < kDepth * kWaves) sm.arrived[0][tid] = sm.finished[0][tid] = 0;
     if (!idle) {
-        load_tables(0);
-        if constexpr (!kDown) load_x(tile_now);
+        look(u0);
         aim(u0);
+        look(u0 + 1);
+        load_tables();
+        if constexpr (!kDown) load_x(tile_now);
         if (!kDown || wave != 0) load_weights();
-        store_tables(0);
-        if constexpr (!kDown) {
-            split_sums();
-            loads_done();
-        }
-    } else {
-        load_tables(0);
-        store_tables(0);
+        if constexpr (!kDown) split_sums();
     }
     if constexpr (kDown) {
-        const int t = tile_of(lo) + lane;  // at most 6 tiles
+        const int t = tile_of(lo) + lane;  // at most 4 tiles
         if (wave == 0 && lo < hi && t * upt < hi)
             if (!wait_for(a.done_gateup + t * kPad, a.I / 16)) give_up(a);
         __syncthreads();
@@ -509,126 +553,152 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
             load_x(tile_now);
             if (wave == 0) load_weights();
             split_sums();
-            loads_done();
         }
-    }
-    const CodeConsts<OFF> kc = code_consts<OFF>(a.zero);
-    __syncthreads();
-    for (int step = 0; step < steps; ++step) {
-        const int u = u0 + step;
-        load_tables(step + 1);
-        if (!idle) {
-            const int tile = tile_of(min(u, u1 - 1));
-            if (tile != tile_now) {
-                tile_now = tile;
-                load_x(tile);
-                split_sums();
-                loads_done();
-            }
-            aim(u + 1);
-            const uint16_t* const ts = sm.tables[step & 1][0] + (32 * wu + lr) * G;
-            const uint16_t* const tb = sm.tables[step & 1][1] + (32 * wu + lr) * G;
-            const int ngl = fresh(ng);
-            f32x4 acc[2];
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int st = 0; st < NS; ++st) {
-                    acc[b] = mfma16(xb[st], table8(tb + 16 * b * G, st, ngl), acc[b]);
-                    if constexpr (OFF != 0) acc[b] = mfma16(xo[st], table8(ts + 16 * b * G, st, ngl), acc[b]);
-                }
-            }
-            constexpr int NB = kBuffers<BITS>;
-#pragma unroll
-            for (int h = 0; h < CPW; h += NB) {
-                // the weights of this unit through LDS, those of the next into their place
-#pragma unroll
-                for (int i = h; i < h + NB && i < CPW; ++i) {
-                    ww.lds = sm.w[wave][i - h];
-                    ww.put(rv[i]);
-                    ww.load(ch0 + i, rv[i]);
-                }
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int i = h; i < h + NB && i < CPW; ++i) {
-                    chunk_fence();  // one chunk's operands at a time: registers
-                    ww.lds = sm.w[wave][i - h];
-                    WLane<BITS> wv[2];
-                    float s[2][CH];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        wv[b] = ww.get(b, lr, q);
-#pragma unroll
-                        for (int j = 0; j < CH; ++j)
-                            s[b][j] = bf16_to_f32(ts[16 * b * G + min(g0 + ((i * CH + j) >> SH), G - 1)]);
-                    }
-                    // columns past the slice have zeros in x
-                    chunk_steps<GS, 2, 4, BITS>(acc, x[i], wv, s, kc);
-                }
-                __builtin_amdgcn_wave_barrier();
-            }
-            // operand rows 8..15 are the lo parts of rows 0..7, in the wave's upper half:
-            // the halves trade places so that the lower one adds up block 0, the upper
-            // one block 1
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const u32x2 t = __builtin_bit_cast(
-                    u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[0][v]), __float_as_uint(acc[1][v]), false, false));
-                sm.red[step & 1][wave][lane >> 5][4 * (q & 1) + v][lr] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
-            }
-        }
-        store_tables(step + 1);
+    } else {
         __syncthreads();
-        // the units' outputs: wave r adds up the shares of row r, 16 columns of both
-        // halves of gate|up by 4 lanes each, 32 of down by 2
-        constexpr int kCols = kDown ? 32 : 16;
-        const int r = wave, c = lane % kCols;
-        for (int i = 0; i < nu; ++i) {
-            const int uu = first(r0 + i) + step;
-            if (uu >= first(r0 + i + 1)) continue;
-            const int t = tile_of(uu), col = uu - t * upt;
-            if (r >= uniform(sm.l.count[t])) continue;
-            const int id = uniform(sm.l.rows[t][r]);
-            const size_t slot = (id >> 6) * a.k + (id & 63);
-            float o[2] = {0.f, 0.f};
-            for (int v = lane / kCols; v < split; v += 64 / kCols) {
-                const auto& red = sm.red[step & 1][(i << log_split) + v];
-                if constexpr (kDown) {
-                    o[0] += red[c >> 4][r][c & 15];
-                } else {
-                    o[0] += red[0][r][c];
-                    o[1] += red[1][r][c];
-                }
-            }
+    }
+    if (!idle) loads_done();
+    const CodeConsts<OFF> kc = code_consts<OFF>(a.zero);
+    // The outputs of the share's unit j: the sums of its waves' shares.
+    auto finish = [&](int j) {
+        const int slot = j % kDepth, u = u0 + j, tile = tile_of(u);
+        if (!wait_lds(&sm.arrived[slot][wu], (j / kDepth + 1) << log_split)) give_up(a);
+        const int count = uniform(sm.l.what[tile]) & 15, col = u - tile * upt;
+        const uint32_t start = uniform(sm.l.start[tile]);
+        const float(*const red)[2][kTileRows][16] = sm.red[slot] + wu * split;
+        if constexpr (kDown) {  // 2 rows of 32 columns at a time
+            const Rsrc ry = make_rsrc(a.y + static_cast<size_t>(start) * a.H, 4u * a.H * count);
+            for (int r0 = 0; r0 < count; r0 += 2) {
+                const int r = r0 + (lane >> 5), c = lane & 31;
+                float o = 0.f;
 #pragma unroll
-            for (int off = kCols; off < 64; off <<= 1) {
-                o[0] += __shfl_xor(o[0], off);
-                if constexpr (!kDown) o[1] += __shfl_xor(o[1], off);
+                for (int v = 0; v < kWaves; ++v) {
+                    const float p = red[min(v, split - 1)][c >> 4][r][c & 15];
+                    o = v < split ? o + p : o;
+                }
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o), ry, 4u * (r * a.H + 32 * col + c), 0, kSc1);
             }
-            if constexpr (kDown) {
-                const Rsrc ry = make_rsrc(a.y + slot * a.H, 4u * a.H);
-                if (lane < kCols)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[0]), ry, 4 * (32 * col + c), 0, kSc1);
-            } else {
+        } else {  // 4 rows of 16 columns, both halves
+            const Rsrc rh = make_rsrc(a.h + static_cast<size_t>(start) * 2 * a.I, 4u * a.I * count);
+            const Rsrc rq = make_rsrc(a.hsum + static_cast<size_t>(start) * 2 * (a.I / 16), 8u * (a.I / 16) * count);
+            for (int r0 = 0; r0 < count; r0 += 4) {
+                const int r = r0 + q, c = lr;
+                float o[2] = {0.f, 0.f};
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p = red[min(v, split - 1)][h][r][c];
+                        o[h] = v < split ? o[h] + p : o[h];
+                    }
                 const float hv = (a.swiglu ? silu(o[0]) : gelu_tanh(o[0])) * o[1];
                 const uint16_t hi16 = f32_to_bf16(hv), lo16 = f32_to_bf16(hv - bf16_to_f32(hi16));
+                const uint32_t at = 2u * (2 * r * a.I + 16 * col + (c & ~7) + permuted_pos(c & 7));
+                __builtin_amdgcn_raw_buffer_store_b16(hi16, rh, at, 0, kSc1);
+                __builtin_amdgcn_raw_buffer_store_b16(lo16, rh, at + 2u * a.I, 0, kSc1);
                 const float shi = sum16(bf16_to_f32(hi16)), slo = sum16(bf16_to_f32(lo16));
-                // lanes 0..15 store the hi parts, 16..31 the lo parts
-                const Rsrc rh = make_rsrc(a.h, 4u * a.I * static_cast<uint32_t>(a.T * a.k));
-                const uint32_t part = 2 * static_cast<uint32_t>(slot) + (lane >> 4);
-                if (lane < 32)
-                    __builtin_amdgcn_raw_buffer_store_b16(lane < 16 ? hi16 : lo16, rh,
-                                                          2u * (part * a.I + 16 * col + (c & 8) + permuted_pos(c & 7)), 0, kSc1);
-                const Rsrc rq = make_rsrc(a.hsum, 8u * (a.I / 16) * static_cast<uint32_t>(a.T * a.k));
-                if (lane == 0 || lane == 16)
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lane ? slo : shi), rq, 4u * (part * (a.I / 16) + col), 0,
-                                                          kSc1);
+                // rows past the count lie past every resource
+                if (c < 2)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(c ? slo : shi), rq,
+                                                          4u * ((2 * r + c) * (a.I / 16) + col), 0, kSc1);
             }
         }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (lane == 0)
+            __hip_atomic_store(&sm.finished[slot][wu], j / kDepth + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    };
+    // The waves of a unit are not in step.  Each leaves its share in one of kDepth
+    // places in turn and counts itself; the waves take turns at making the outputs,
+    // kLag units later, when all shares are there as a rule, and count that too: then
+    // the place may be written again.
+    for (int it = 0; it < u1 - u0 + kLag; ++it) {
+        if (it >= kLag && ((it - kLag) & (split - 1)) == ws) finish(it - kLag);
+        const int u = u0 + it;
+        if (u >= u1) continue;
+        const int tile = tile_of(u);
+        if (tile != tile_now) {
+            tile_now = tile;
+            load_x(tile);
+            split_sums();
+            loads_done();
+        }
+        store_tables();
+        aim(u + 1);
+        load_tables();
+        look(u + 2);
+        const int free = __hip_atomic_load(&sm.finished[it % kDepth][wu], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        const int ngl = fresh(ng);
+        u32x4 sc[2][NS];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int st = 0; st < NS; ++st) sc[b][st] = table8(0, b, st, ngl);
+        // chunk i of this unit into its buffer, of the next unit into its registers
+        constexpr bool kAll = CPW <= kBuffers<BITS>;
+        auto turn = [&](int i) {
+            ww.lds = sm.w[wave][i % kBuffers<BITS>];
+            ww.put(rv[i]);
+            ww.load(chunk(i), rv[i]);
+        };
+        f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < (kAll ? CPW : 1); ++i) turn(i);
+#pragma unroll
+        for (int i = 0; i < CPW; ++i) {
+            if (!kAll || i == 0) {
+                chunk_fence();
+                if (!kAll && i + 1 < CPW) turn(i + 1);
+                __builtin_amdgcn_wave_barrier();
+            }
+            ww.lds = sm.w[wave][i % kBuffers<BITS>];
+            WLane<BITS> wv[2];
+            float s16[2][CH];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                wv[b] = ww.get(b, lr, q);
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    const int g = (i * CH + j) >> SH;
+                    const uint32_t pair = sc[b][g >> 3][(g & 7) >> 1];
+                    s16[b][j] = __uint_as_float(g & 1 ? pair & 0xFFFF0000u : pair << 16);
+                }
+            }
+            // columns past the slice have zeros in x
+            chunk_steps<GS, 2, 4, BITS>(acc, x[i], wv, s16, kc);
+            if (!kAll || i + 1 == CPW) __builtin_amdgcn_wave_barrier();
+        }
+        // + sum_g b X - OFF s X
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            f32x4& o = acc[b];
+            f32x4 sx = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < NS; ++st) {
+                o = mfma16(xb[st], table8(1, b, st, ngl), o);
+                if constexpr (OFF != 0) sx = mfma16(xb[st], sc[b][st], sx);
+            }
+            if constexpr (OFF != 0) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) o[v] = fmaf(-static_cast<float>(OFF), sx[v], o[v]);
+            }
+        }
+        const int slot = it % kDepth;
+        if (uniform(free) < it / kDepth && !wait_lds(&sm.finished[slot][wu], it / kDepth)) give_up(a);
+        // operand rows 8..15 are the lo parts of rows 0..7, in the wave's upper half:
+        // the halves of two blocks trade places so that the lower half adds up the
+        // first one, the upper half the second
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const u32x2 t = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[0][v]), __float_as_uint(acc[1][v]), false, false));
+            sm.red[slot][wave][lane >> 5][4 * (q & 1) + v][lr] = __uint_as_float(t[0]) + __uint_as_float(t[1]);
+        }
+        asm volatile("" ::: "memory");  // the LDS operations of a wave keep their order
+        if (lane == 0) __hip_atomic_fetch_add(&sm.arrived[slot][wu], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     // the range is done once its stores have been acknowledged; the phase's flags
     // are read meanwhile
+    static_assert(kRanges <= kFewThreads, "a flag a thread");
     const int taken = tid < kRanges ? __hip_atomic_load(flags + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 1;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     const bool left = __syncthreads_or(!taken);
@@ -640,11 +710,12 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     return left;
 }
 
-// The same with the chunks of a wave's slice known: 3, or 4.
+// The same with the chunks of a wave's slice known: up to 2, 3 or 4.
 template <int GS, int BITS, bool kDown>
 __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>& sm, int range, const int32_t* flags) {
     const int nch = ((kDown ? a.I : a.H) + 127) / 128;
     const int log_split = split_log(nch), most = (nch + (1 << log_split) - 1) >> log_split;
+    if (most <= 2) return run_range<GS, BITS, kDown, 2>(a, sm, range, flags);
     return most <= 3 ? run_range<GS, BITS, kDown, 3>(a, sm, range, flags)
                      : run_range<GS, BITS, kDown, 4>(a, sm, range, flags);
 }
@@ -652,38 +723,49 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
 // out and normed of one token.
 template <int GS, int BITS>
 __device__ __forceinline__ void finish_token(const LayerArgs& a, FewSmem<GS, BITS>& sm, int t) {
+    constexpr int NV = 4096 / (8 * kFewThreads), kStep = 8 * kFewThreads;
     const int c0 = 8 * threadIdx.x, k = a.k, H = a.H;
-    norm::Row<kWaves, 1, 8, -1> row;
+    norm::Row<kWaves, NV, 8, -1> row;
     row.load(a.tail, t, c0);
     if (static_cast<int>(threadIdx.x) < k)  // lanes of the first wave
         if (!wait_for(a.done_down + sm.l.slot_tile[t * k + threadIdx.x] * kPad, H / 32)) give_up(a);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     const int failed = __hip_atomic_load(a.failed, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    float z[1][8] = {};
-    const Rsrc ry = make_rsrc(a.y + static_cast<size_t>(t) * k * H, 4u * H * k);
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        u32x4 v[8][2];
+    float z[NV][8] = {};
+    const Rsrc ry = make_rsrc(a.y, 4u * H * static_cast<uint32_t>(a.T * k));
+    constexpr int J = 8;  // experts in flight
+    for (int j0 = 0; j0 < k; j0 += J) {
+        u32x4 v[J][NV][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < J; ++j) {
+            const uint32_t row = sm.l.slot_row[t * k + min(j0 + j, k - 1)];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t at = j0 + j < k && c0 < H ? 4u * ((j0 + j) * H + c0 + 4 * h) : 0xFFFFFFF0u;
-                v[j][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, kSc1));
-            }
+            for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float wt = j0 + j < k ? sm.l.weight[t * k + j0 + j] : 0.f;
+                for (int h = 0; h < 2; ++h) {
+                    const int c = c0 + kStep * i;
+                    const uint32_t at = c < H ? 4u * (row * H + c + 4 * h) : 0xFFFFFFF0u;
+                    v[j][i][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ry, at, 0, kSc1));
+                }
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p = wt * __uint_as_float(v[j][i >> 2][i & 3]);
-                z[0][i] = j0 + j < k ? z[0][i] + p : z[0][i];
-            }
+        for (int j = 0; j < J; ++j) {
+            const float wt = sm.l.weight[t * k + min(j0 + j, k - 1)];
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float p = wt * __uint_as_float(v[j][i][n >> 2][n & 3]);
+                    z[i][n] = j0 + j < k ? z[i][n] + p : z[i][n];
+                }
         }
     }
     if (failed) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[0][i] = __uint_as_float(0x7FC00000u);
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) z[i][n] = __uint_as_float(0x7FC00000u);
     }
     row.finish(a.tail, t, c0, z, sm.lds);
 }
@@ -693,10 +775,10 @@ __global__ __launch_bounds__(kFewThreads, 1) void moe_layer_few_experts(LayerArg
     __shared__ FewSmem<GS, BITS> sm;
     make_lists(a, sm);
     // usually one range of each phase; more if workgroups have not started yet
-    for (int r = sm.own[0] ? blockIdx.x : take(sm, a.claim_gateup, kRanges); r >= 0;)
-        r = run_range<GS, BITS, false>(a, sm, r, a.claim_gateup) ? take(sm, a.claim_gateup, kRanges) : -1;
-    for (int r = sm.own[1] ? blockIdx.x : take(sm, a.claim_down, kRanges); r >= 0;)
-        r = run_range<GS, BITS, true>(a, sm, r, a.claim_down) ? take(sm, a.claim_down, kRanges) : -1;
+    for (int r = sm.own[0] ? blockIdx.x : take(sm, a.claim_gateup); r >= 0;)
+        r = run_range<GS, BITS, false>(a, sm, r, a.claim_gateup) ? take(sm, a.claim_gateup) : -1;
+    for (int r = sm.own[1] ? blockIdx.x : take(sm, a.claim_down); r >= 0;)
+        r = run_range<GS, BITS, true>(a, sm, r, a.claim_down) ? take(sm, a.claim_down) : -1;
     if (static_cast<int>(blockIdx.x) < a.T) finish_token(a, sm, blockIdx.x);
 }
 

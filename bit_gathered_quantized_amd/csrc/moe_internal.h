@@ -320,7 +320,7 @@ struct LayerArgs {
     bool swiglu, norm, norm_f32;
     float eps, weight_offset;
     uint32_t zero;  // always 0 (see CodeConsts)
-    uint32_t magic_gateup, magic_down;  // 2^32 / units of a tile, rounded up
+    uint32_t magic_gateup, magic_down;  // 2^31 / units of a tile, rounded up
     RouterArgs router;
     const float* expert_scale;
     const uint16_t* x;
@@ -339,7 +339,7 @@ struct LayerArgs {
     float* logits;       // [T, E]
     uint16_t* n;         // [T, 2, H]: rms(x) as bf16 hi and lo, pieces permuted
     float* nsum;         // [T, 2, H / gs]: their sums over groups
-    uint16_t* h;         // [T * k, 2, I]
+    uint16_t* h;         // [T * k, 2, I]; rows of h, hsum and y in the order of the tiles
     float* hsum;         // [T * k, 2, I / 16]: sums over 16 columns
     float* y;            // [T * k, H]
 };

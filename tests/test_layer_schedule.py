@@ -7,11 +7,12 @@ import random
 import pytest
 
 RANGES, WAVES, CHUNKS, THREADS, ROWS = 256, 8, 4, 512, 8
+DEPTH, LAG = 4, 2
 
 
 def geometry(K, gs, bits):
     nch = (K + 127) // 128
-    log_split = 0 if nch <= 4 else 1 if nch <= 8 else 2 if nch <= 16 else 3
+    log_split = 0 if nch <= 3 else 1 if nch <= 6 else 2 if nch <= 12 else 3
     return nch, log_split, 1 << log_split, WAVES >> log_split
 
 
@@ -56,20 +57,30 @@ def test_units_and_indices(T, k, E, H, I, gs, bits, down):
         assert nc <= CHUNKS
         cover += range(c0, c0 + nc)
     assert cover == list(range(nch))
-    # tables: pieces of 16 bytes, two a thread, inside the buffer
-    assert nu * 8 * G <= 2 * THREADS and nu * 64 * G <= 8 * 4096 // gs * 8
-    assert (16 * G * 2) % 16 == 0
-    # chain sums
-    chain = 32 if gs == 32 else 64
-    per_chunk = 128 // chain
-    assert CHUNKS * per_chunk * 16 == 64 * per_chunk
+    # a wave's table rows: lanes (block, row, piece) cover the slice from the piece in
+    # which it begins, and the reads of 8 entries stay in the row
+    pieces = 2 if 512 // gs <= 8 else 4
+    rows = E * (H if down else 2 * I)
+    for ws in range(split):
+        c0 = nch * ws >> log_split
+        nc = (nch * (ws + 1) >> log_split) - c0
+        g0, ng = c0 * 128 // gs, min(nc * 128 // gs, G - c0 * 128 // gs)
+        steps8 = (max(2, -(-nch // split)) * 128 // gs + 7) // 8
+        for lr in range(16):
+            sub = 2 * (lr * G + g0) & 15
+            assert sub + 2 * ng <= 16 * pieces and sub + 16 * steps8 <= 16 * pieces and ng <= 8 * steps8
+            for base in (0, rows - 16):  # the same piece for all units
+                assert 2 * ((base + lr) * G + g0) & 15 == sub
+    # units to tiles by a multiplication
+    m = -(-2**31 // upt)
+    for u in {0, upt - 1, upt, N - 1, max(N - upt, 0), max(N - upt - 1, 0), N // 2}:
+        assert m < 2**32 and 2 * u * m >> 32 == u // upt
     done, seen = [0] * len(tiles), 0
     for r in range(RANGES):
         lo, hi = first(r * nu), first((r + 1) * nu)
-        steps = max(first(r * nu + i + 1) - first(r * nu + i) for i in range(nu))
         for i in range(nu):
             u0, u1 = first(r * nu + i), first(r * nu + i + 1)
-            assert lo <= u0 <= u1 <= hi and u1 - u0 <= steps
+            assert lo <= u0 <= u1 <= hi
             for u in range(u0, u1):
                 seen += 1
                 tile, c = divmod(u, upt)
@@ -85,36 +96,68 @@ def test_units_and_indices(T, k, E, H, I, gs, bits, down):
                 if t0 * upt < hi:
                     done[t0] += min(hi, (t0 + 1) * upt) - max(lo, t0 * upt)
     assert seen == N and done == [upt] * len(tiles)
-    # outputs: threads over rows and columns
-    out = 256 if down else 128
-    for p in {0, 1, out - 1, nu * out - 1}:
-        i, rr, c = p // out, p // (out // ROWS) % ROWS, p % (out // ROWS)
-        assert i < nu and rr < ROWS and c < (32 if down else 16)
 
 
-def run_order(T, tiles, slots_tile, resident, rng, ranges=12):
+@pytest.mark.parametrize("split", [1, 2, 4, 8])
+def test_shares_of_a_unit(split):
+    """The waves of a unit, scheduled at random: every unit's outputs are made once,
+    after all its shares and before their place is written again."""
+    for units in range(24):
+        for seed in range(4):
+            rng = random.Random(seed)
+            arrived, finished, outputs = [0] * DEPTH, [0] * DEPTH, []
+            place = [[None] * split for _ in range(DEPTH)]
+
+            def wave(ws):
+                for it in range(units + LAG):
+                    j = it - LAG
+                    if j >= 0 and j % split == ws:
+                        while arrived[j % DEPTH] < (j // DEPTH + 1) * split:
+                            yield False
+                        assert place[j % DEPTH] == [j] * split
+                        yield True
+                        assert place[j % DEPTH] == [j] * split
+                        outputs.append(j)
+                        finished[j % DEPTH] = j // DEPTH + 1
+                    if it < units:
+                        while finished[it % DEPTH] < it // DEPTH:
+                            yield False
+                        place[it % DEPTH][ws] = it
+                        yield True
+                        arrived[it % DEPTH] += 1
+
+            live, idle = {w: wave(w) for w in range(split)}, 0
+            while live:
+                w = rng.choice(sorted(live))
+                try:
+                    idle = 0 if next(live[w]) else idle + 1
+                except StopIteration:
+                    del live[w]
+                    idle = 0
+                assert idle < 1000, "no wave gets on"
+            assert sorted(outputs) == list(range(units))
+
+
+def run_order(T, tiles, slots_tile, resident, rng, ranges=20):
     """Workgroups as generators, only `resident` of them started at a time and the
     scheduler picking one at random; returns the steps taken."""
-    flags = {"gu": [0] * ranges, "dn": [0] * ranges, "tok": [0] * T}
+    flags = {"gu": [0] * ranges, "dn": [0] * ranges}
     units = {"gu": 5, "dn": 7}
     done = {"gu": [0] * tiles, "dn": [0] * tiles}
     outputs = [0] * T
 
-    def take(name, own):
-        n = len(flags[name])
-        if own is not None:
-            yield
-            if not flags[name][own]:
-                flags[name][own] = 1
-                return own
+    def claim(name, r):
+        won, flags[name][r] = not flags[name][r], 1
+        return won
+
+    def take(name):  # any untaken range
         while True:
             yield
-            free = [i for i in range(n) if not flags[name][i]]
+            free = [i for i in range(ranges) if not flags[name][i]]
             if not free:
                 return None
             yield
-            if not flags[name][free[0]]:
-                flags[name][free[0]] = 1
+            if claim(name, free[0]):
                 return free[0]
 
     def span(name, r):
@@ -122,24 +165,27 @@ def run_order(T, tiles, slots_tile, resident, rng, ranges=12):
         return range(N * r // ranges, N * (r + 1) // ranges)
 
     def group(b):
+        own = {}
+        for name in ("gu", "dn"):  # both of its own at once
+            yield
+            own[name] = claim(name, b)
         for name in ("gu", "dn"):
-            r = yield from take(name, b)
+            r = b if own[name] else (yield from take(name))
             while r is not None:
-                for u in span(name, r):
-                    if name == "dn":
-                        while done["gu"][u // units["dn"]] < units["gu"]:
+                if name == "dn":  # one wait for all tiles of the range
+                    for tile in {u // units["dn"] for u in span(name, r)}:
+                        while done["gu"][tile] < units["gu"]:
                             yield "wait"
+                for u in span(name, r):
                     yield
                 for u in span(name, r):
                     done[name][u // units[name]] += 1
-                r = yield from take(name, None)
-        t = yield from take("tok", b % T)
-        while t is not None:
-            for tile in slots_tile[t]:
+                r = yield from take(name)
+        if b < T:  # workgroup t finishes token t
+            for tile in slots_tile[b]:
                 while done["dn"][tile] < units["dn"]:
                     yield "wait"
-            outputs[t] += 1
-            t = yield from take("tok", None)
+            outputs[b] += 1
 
     waiting, live, steps, idle = [group(b) for b in range(ranges)], [], 0, 0
     while waiting or live:
