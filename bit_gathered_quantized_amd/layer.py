@@ -38,10 +38,16 @@ class MoeRouter(ctypes.Structure):
                 ("weight", ctypes.c_void_p), ("expert_scale", ctypes.c_void_p)]
 
 
+_package = None
+
+
 def _api():
     """The package (imported late: it imports this module)."""
-    import bit_gathered_quantized_amd as bgq
-    return bgq
+    global _package
+    if _package is None:
+        import bit_gathered_quantized_amd as bgq
+        _package = bgq
+    return _package
 
 
 def _type(t, name):
@@ -67,20 +73,27 @@ def _device(t, name):
 def _rows(t, name, dev, T, H):
     """Row stride of a [T, H] tensor whose rows are contiguous."""
     _on(t, name, dev)
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H:
+    if t.shape != (T, H):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H)}")
-    if t.stride(1) != 1 and H > 1:
+    st, sh = t.stride()
+    if sh != 1 and H > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
-    return t.stride(0) if T > 1 else max(H, 1)
+    return st if T > 1 else max(H, 1)
 
 
 def _vector(t, name, dev, n):
     _on(t, name, dev)
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n,)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
+
+
+def _like(t):
+    """A new contiguous tensor of t's shape and type."""
+    import torch
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 @contextlib.contextmanager
@@ -113,16 +126,18 @@ def _gate(n, gate, dev, T, H):
         return
     _on(gate, "gate", dev)
     n.gate_type = _type(gate, "gate")
-    try:
-        g = gate.expand(T, H)
-    except RuntimeError:
-        raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}") from None
-    st, sh = g.stride()
+    if gate.shape == (H,):
+        st, (sh,) = 0, gate.stride()
+    else:
+        try:
+            st, sh = gate.expand(T, H).stride()
+        except RuntimeError:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, which does not broadcast to {(T, H)}") from None
     if H == 1:
         sh = 0
     if sh not in (0, 1):
         raise ValueError("gate must be contiguous or broadcast along H")
-    n.gate, n.gate_stride_t, n.gate_stride_h = g.data_ptr(), st if T > 1 else 0, sh
+    n.gate, n.gate_stride_t, n.gate_stride_h = gate.data_ptr(), st if T > 1 else 0, sh
 
 
 def _norm_tail(n, T, H, dev, residual, post_norm, post_weight, gate, residual_scale, pre_norm, pre_weight,
@@ -193,14 +208,17 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None
         o, m = out, normed
         if want_out:
             if o is None:
-                o = torch.empty((T, H), dtype=dtype, device=dev)
-            n.out_stride = _rows(o, "out", dev, T, H)
+                o = _like(y if residual is None else residual)
+                n.out_stride = H
+            else:
+                n.out_stride = _rows(o, "out", dev, T, H)
             n.out = o.data_ptr()
         if with_normed:
             if m is None:
-                m = torch.empty((T, H), dtype=dtype, device=dev)
-            n.normed_type = _type(m, "normed")
-            n.normed_stride = _rows(m, "normed", dev, T, H)
+                m = _like(y if residual is None else residual)
+                n.normed_type, n.normed_stride = _type(m, "normed"), H
+            else:
+                n.normed_type, n.normed_stride = _type(m, "normed"), _rows(m, "normed", dev, T, H)
             n.normed = m.data_ptr()
         st = bgq.lib().moe_block_norm(ctypes.byref(n), y.data_ptr(), raw)
         if st != 0:
@@ -216,6 +234,15 @@ def _output(t, name, dev, shape, dtype):
     if tuple(t.shape) != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
     return t.data_ptr()
+
+
+def _new_or_given(t, name, dev, shape, dtype):
+    """The output, allocated unless given, and its data pointer."""
+    import torch
+    if t is not None:
+        return t, _output(t, name, dev, shape, dtype)
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    return t, t.data_ptr()
 
 
 def router_forward(x, weight, k, *, norm=True, eps=1e-6, expert_scale=None, logits=None, ids=None, weights=None,
@@ -255,17 +282,10 @@ def router_forward(x, weight, k, *, norm=True, eps=1e-6, expert_scale=None, logi
         raise ValueError(f"k must be between 1 and the number of experts {E}, got {k}")
 
     def go(raw):
-        lo, i, w = logits, ids, weights
-        if lo is None:
-            lo = torch.empty((T, E), dtype=torch.float32, device=dev)
-        if i is None:
-            i = torch.empty((T, k), dtype=torch.int32, device=dev)
-        if w is None:
-            w = torch.empty((T, k), dtype=torch.float32, device=dev)
-        st = bgq.lib().moe_router_forward(ctypes.byref(r), x.data_ptr(),
-                                          _output(lo, "logits", dev, (T, E), torch.float32),
-                                          _output(i, "ids", dev, (T, k), torch.int32),
-                                          _output(w, "weights", dev, (T, k), torch.float32), raw)
+        lo, plo = _new_or_given(logits, "logits", dev, (T, E), torch.float32)
+        i, pi = _new_or_given(ids, "ids", dev, (T, k), torch.int32)
+        w, pw = _new_or_given(weights, "weights", dev, (T, k), torch.float32)
+        st = bgq.lib().moe_router_forward(ctypes.byref(r), x.data_ptr(), plo, pi, pw, raw)
         if st != 0:
             raise bgq.MoeError(st, "moe_router_forward")
         return lo, i, w
@@ -399,13 +419,18 @@ class MoeLayer:
         def go(raw):
             o, m, ws = out, normed, workspace
             if o is None:
-                o = torch.empty((T, H), dtype=dtype, device=dev)
-            n.out_stride, n.out = _rows(o, "out", dev, T, H), o.data_ptr()
+                o = _like(x if residual is None else residual)
+                n.out_stride = H
+            else:
+                n.out_stride = _rows(o, "out", dev, T, H)
+            n.out = o.data_ptr()
             if self._pre:
                 if m is None:
-                    m = torch.empty((T, H), dtype=dtype, device=dev)
-                n.normed_type = _type(m, "normed")
-                n.normed_stride, n.normed = _rows(m, "normed", dev, T, H), m.data_ptr()
+                    m = _like(out if out is not None else x if residual is None else residual)
+                    n.normed_type, n.normed_stride = _type(m, "normed"), H
+                else:
+                    n.normed_type, n.normed_stride = _type(m, "normed"), _rows(m, "normed", dev, T, H)
+                n.normed = m.data_ptr()
             if ws is None:
                 need = bgq.lib().moe_layer_workspace_bytes(ctypes.byref(p))
                 ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
