@@ -59,7 +59,8 @@ __device__ __forceinline__ void split3(u32x4 a, u32x4 b, u32x4 (&p)[3]) {
 }
 
 // MT row blocks of 16 tokens, NT of 16 experts, WAVES cuts of the columns; each
-// wave keeps the operands of RING steps of 32 columns in flight.
+// wave keeps the operands of RING steps of 32 columns in flight (measured: of 16 x 16
+// tiles 2 9.8, 4 10.4, 6 10.1 us at 512 tokens; of the larger ones more cost more).
 template <int MT, int NT, int WAVES, int RING, bool kWF32>
 __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs a) {
     constexpr int kRows = 16 * MT, kExperts = 16 * NT, kW = kWF32 ? 4 : 2, kRaw = kWF32 ? 2 : 1, kParts = kWF32 ? 3 : 1;
@@ -85,8 +86,9 @@ __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs
     const int rows = min(kRows, a.T - t0), experts = min(kExperts, E - e0);
     // rows past the batch and experts past E read zeros
     const uint32_t xrow = 2u * static_cast<uint32_t>(a.x_stride), wrow = static_cast<uint32_t>(H) * kW;
-    const Rsrc rx = make_rsrc(a.x + t0 * a.x_stride, (rows - 1) * xrow + 2u * H);
-    const Rsrc rw = make_rsrc(static_cast<const char*>(a.weight) + static_cast<size_t>(e0) * wrow, experts * wrow);
+    const void* const px = a.x + t0 * a.x_stride;
+    const void* const pw = static_cast<const char*>(a.weight) + static_cast<size_t>(e0) * wrow;
+    const uint32_t nx = (rows - 1) * xrow + 2u * H, nw = experts * wrow;
 
     f32x4 acc[MT][NT], gram[MT];
 #pragma unroll
@@ -106,7 +108,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs
     const uint32_t wat = kWF32 ? r8 * wrow + 16u * p8 : r4 * wrow + 16u * p4;
     const int put4 = 4 * r4 + (p4 ^ (r4 >> 2 & 3)), get4 = 4 * lr + (q ^ (lr >> 2 & 3));
     u32x4 x[RING][MT], raw[RING][NT][kRaw];
+    // Past the wave's share zeros are read, and multiplied: with a branch around the
+    // product the compiler waits for every load under way.
     auto load = [&](int slot, int s) {
+        const Rsrc rx = make_rsrc(px, s < s1 ? nx : 0), rw = make_rsrc(pw, s < s1 ? nw : 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -152,13 +157,12 @@ __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs
         for (int m = 0; m < MT; ++m) gram[m] = mfma16(xo[m], xo[m], gram[m]);
     };
 #pragma unroll
-    for (int i = 0; i < RING; ++i) load(i, min(s0 + i, steps - 1));
+    for (int i = 0; i < RING; ++i) load(i, s0 + i);
     for (int s = s0; s < s1; s += RING) {
 #pragma unroll
         for (int i = 0; i < RING; ++i) {
-            if (s + i < s1) compute(i);
-            // past the wave's share the last step is read again, for nothing
-            load(i, min(s + i + RING, steps - 1));
+            compute(i);
+            load(i, s + i + RING);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -222,17 +226,21 @@ hipError_t launch_router_product(const RouterArgs& a, hipStream_t s) {
         few<4>(a, s);
     else if (T <= 8)
         few<8>(a, s);
-    // the largest tile that still gives every CU (32 x 32: every other) a workgroup.
-    // Measured with top-k,
-    // 64 x 64 | 32 x 32 | 16 x 16: 8192 tokens and 128 experts 29 | 46 | 105 us,
-    // 2048 and 128 22 | 14 | 26 us, 512 and 128 18 | 11.3 | 11.2 us (fp32 weights
-    // 28 | 16 | 13 us), 64 and 128 (fp32) 24 | 15 | 10 us
-    else if (groups(4, 4) >= 256)
+    // the largest tile that still gives every other CU a workgroup.  Measured with top-k,
+    // 64 x 64 | 32 x 32 | 16 x 16, 128 experts: 8192 tokens 35 | 46 | 105 us, 5120
+    // 29.4 | 36.3 us, 4096 29.9 | 29.4 us, 2048 22 | 14 | 26 us, 512 18 | 11.3 | 9.8 us
+    // (fp32 weights 28 | 16 | 13 us), 64 (fp32) 24 | 15 | 10 us.  With more than one
+    // 64 x 64 workgroup a CU two of four waves at a time, so that one starts or ends
+    // while the other multiplies, not one of eight (4001 tokens and 512 experts 53 | 58
+    // us; 8192 and 128, one to a CU, 42 | 35 us)
+    else if (groups(4, 4) > 256)
+        tile<4, 4, 4, 1>(a, s);
+    else if (groups(4, 4) > 128)
         tile<4, 4, 8, 1>(a, s);
     else if (groups(2, 2) >= 128)
         tile<2, 2, 8, 2>(a, s);
     else
-        tile<1, 1, 16, 4>(a, s);
+        tile<1, 1, 16, 2>(a, s);
     return hipGetLastError();
 }
 

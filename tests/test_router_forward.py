@@ -101,6 +101,18 @@ def test_sizes(wt, T, E, H, k):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("wt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,E,H,k", [(1037, 1024, 128, 8), (257, 1000, 64, 3), (4201, 128, 192, 8), (8321, 100, 64, 4),
+                                     (129, 70, 320, 2)])
+def test_large_tiles_and_their_order(wt, T, E, H, k):
+    """Batches of the largest tiles, with four and with eight waves, grouped by XCD
+    (with blocks past the batch) and not."""
+    x, w, scale = make(T, E, H, wt)
+    check(x, w, k, None, bgq.router_forward(x, w, k))
+    check(x, w, k, scale, bgq.router_forward(x, w, k, expert_scale=scale))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [7, 300])
 def test_without_norm_strided_rows_and_given_outputs(T):
     x, w, scale = make(T, 24, 320, torch.float32, seed=3)
