@@ -58,10 +58,11 @@ __device__ __forceinline__ void split3(u32x4 a, u32x4 b, u32x4 (&p)[3]) {
     }
 }
 
-// MT row blocks of 16 tokens, NT of 16 experts, WAVES cuts of the columns; each
-// wave keeps the operands of RING steps of 32 columns in flight (measured: of 16 x 16
-// tiles 2 9.8, 4 10.4, 6 10.1 us at 512 tokens; of the larger ones more cost more).
-template <int MT, int NT, int WAVES, int RING, bool kWF32>
+// MT row blocks of 16 tokens, NT of 16 experts, WAVES cuts of the columns.  A wave has
+// the operands of one step of 32 columns in flight: the other waves fill the time, and
+// more steps measured slower (16 x 16 with fp32 weights at 512 tokens, 1 | 2 steps 10.6
+// | 11.3 us; 32 x 32 at 2048, 1 | 2 | 3 steps 16.9 | 18.1 | 19.5 us).
+template <int MT, int NT, int WAVES, bool kWF32>
 __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs a) {
     constexpr int kRows = 16 * MT, kExperts = 16 * NT, kW = kWF32 ? 4 : 2, kRaw = kWF32 ? 2 : 1, kParts = kWF32 ? 3 : 1;
     // wave-private turning buffers in the loop, then the waves' sums
@@ -107,32 +108,31 @@ __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs
     const uint32_t xat = r4 * xrow + 16u * p4;
     const uint32_t wat = kWF32 ? r8 * wrow + 16u * p8 : r4 * wrow + 16u * p4;
     const int put4 = 4 * r4 + (p4 ^ (r4 >> 2 & 3)), get4 = 4 * lr + (q ^ (lr >> 2 & 3));
-    u32x4 x[RING][MT], raw[RING][NT][kRaw];
-    // Past the wave's share zeros are read, and multiplied: with a branch around the
-    // product the compiler waits for every load under way.
-    auto load = [&](int slot, int s) {
+    u32x4 x[MT], raw[NT][kRaw];
+    // past the wave's share nothing is read
+    auto load = [&](int s) {
         const Rsrc rx = make_rsrc(px, s < s1 ? nx : 0), rw = make_rsrc(pw, s < s1 ? nw : 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < kRaw; ++h)
-                raw[slot][n][h] = load16(rw, wat + (16u * n + 8u * h) * wrow + 32u * kW * s);
+                raw[n][h] = load16(rw, wat + (16u * n + 8u * h) * wrow + 32u * kW * s);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) x[slot][m] = load16(rx, xat + 16u * m * xrow + 64u * s);
+        for (int m = 0; m < MT; ++m) x[m] = load16(rx, xat + 16u * m * xrow + 64u * s);
     };
-    auto compute = [&](int slot) {
+    auto compute = [&] {
         u32x4 (&buf)[MT + NT * kRaw][64] = sm.turn[wave];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if constexpr (kWF32) {  // rows of 8 pieces over two buffers, row r8 + 8 h
 #pragma unroll
-                for (int h = 0; h < 2; ++h) buf[MT + 2 * n + h][8 * r8 + (p8 ^ ((r8 + 8 * h) >> 1 & 7))] = raw[slot][n][h];
+                for (int h = 0; h < 2; ++h) buf[MT + 2 * n + h][8 * r8 + (p8 ^ ((r8 + 8 * h) >> 1 & 7))] = raw[n][h];
             } else {
-                buf[MT + n][put4] = raw[slot][n][0];
+                buf[MT + n][put4] = raw[n][0];
             }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m) buf[m][put4] = x[slot][m];
+        for (int m = 0; m < MT; ++m) buf[m][put4] = x[m];
         __builtin_amdgcn_wave_barrier();
         u32x4 w[NT][kParts], xo[MT];
 #pragma unroll
@@ -156,15 +156,11 @@ __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs
 #pragma unroll
         for (int m = 0; m < MT; ++m) gram[m] = mfma16(xo[m], xo[m], gram[m]);
     };
-#pragma unroll
-    for (int i = 0; i < RING; ++i) load(i, s0 + i);
-    for (int s = s0; s < s1; s += RING) {
-#pragma unroll
-        for (int i = 0; i < RING; ++i) {
-            compute(i);
-            load(i, s + i + RING);
-            __builtin_amdgcn_sched_barrier(0);
-        }
+    load(s0);
+    for (int s = s0; s < s1; ++s) {
+        compute();
+        load(s + 1);
+        __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();  // the turning buffers become the sums
     // lane (lr, q) holds rows 4 q + v and column lr of each 16 x 16 product
@@ -198,7 +194,7 @@ void few(const RouterArgs& a, hipStream_t s) {
     else
         hipLaunchKernelGGL((moe_router_product_few<TM, false>), dim3(a.E), dim3(256), 0, s, a);
 }
-template <int MT, int NT, int WAVES, int RING>
+template <int MT, int NT, int WAVES>
 void tile(const RouterArgs& a, hipStream_t s) {
     const uint32_t down = (static_cast<uint32_t>(a.T) + 16 * MT - 1) / (16 * MT), across = (a.E + 16 * NT - 1) / (16 * NT);
     // By XCD where x would be read often and every XCD has its share.  By XCD | not:
@@ -207,9 +203,9 @@ void tile(const RouterArgs& a, hipStream_t s) {
     const bool by_xcd = across > 4 && down >= 8 && down <= 8 * 65535;
     const dim3 grid(by_xcd ? 8 : down, across, by_xcd ? (down + 7) / 8 : 1), block(64 * WAVES);
     if (a.weight_f32)
-        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, RING, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, true>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, RING, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((moe_router_product_tile<MT, NT, WAVES, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -228,19 +224,19 @@ hipError_t launch_router_product(const RouterArgs& a, hipStream_t s) {
         few<8>(a, s);
     // the largest tile that still gives every other CU a workgroup.  Measured with top-k,
     // 64 x 64 | 32 x 32 | 16 x 16, 128 experts: 8192 tokens 35 | 46 | 105 us, 5120
-    // 29.4 | 36.3 us, 4096 29.9 | 29.4 us, 2048 22 | 14 | 26 us, 512 18 | 11.3 | 9.8 us
+    // 29.4 | 34 us, 4096 29.9 | 27 us, 2048 22 | 14 | 26 us, 512 18 | 11.3 | 9.8 us
     // (fp32 weights 28 | 16 | 13 us), 64 (fp32) 24 | 15 | 10 us.  With more than one
     // 64 x 64 workgroup a CU two of four waves at a time, so that one starts or ends
     // while the other multiplies, not one of eight (4001 tokens and 512 experts 53 | 58
     // us; 8192 and 128, one to a CU, 42 | 35 us)
     else if (groups(4, 4) > 256)
-        tile<4, 4, 4, 1>(a, s);
+        tile<4, 4, 4>(a, s);
     else if (groups(4, 4) > 128)
-        tile<4, 4, 8, 1>(a, s);
+        tile<4, 4, 8>(a, s);
     else if (groups(2, 2) >= 128)
-        tile<2, 2, 8, 2>(a, s);
+        tile<2, 2, 8>(a, s);
     else
-        tile<1, 1, 16, 2>(a, s);
+        tile<1, 1, 16>(a, s);
     return hipGetLastError();
 }
 
