@@ -381,10 +381,11 @@ class MoeLayer:
                  workspace=None, stream=None):
         """The layer on x bf16 [T, H].  residual, gate and residual_scale as for
         block_norm (rows of residual, out, normed and a [T, H] gate start on 16
-        bytes); out and normed default to the residual's type (x's without one).  ids
-        (int32) and weights (fp32), [T, k], receive the routing if given.  workspace:
-        a uint8 tensor of workspace_bytes(T) bytes, one per call at a time (allocated
-        if None).  Returns out, or (out, normed) if the layer norms its output."""
+        bytes); out and normed default to the residual's type (x's without one), and one
+        of them may be x or the residual itself.  ids (int32) and weights (fp32),
+        [T, k], receive the routing if given.  workspace: a uint8 tensor of
+        workspace_bytes(T) bytes, one per call at a time (allocated if None).  Returns
+        out, or (out, normed) if the layer norms its output."""
         import torch
         bgq = _api()
         dev, H, k = self.device, self.H, self.k

@@ -281,6 +281,23 @@ def test_repeats_streams_and_rows(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T", [1, 11, 16, 40])
+def test_in_place(T, norm):
+    """out, or normed, is x itself, which is the residual as well."""
+    w = make(12, 320, 192, seed=T)
+    layer = layer_of(w, 3, norm=norm, norm_weight=w["norm"] if norm else None, post_weight=w["post"], pre_weight=w["pre"])
+    x = tokens(w, T)
+    out, normed = layer(x, residual=x, gate=w["post"])
+    a = x.clone()
+    o, n = layer(a, residual=a, gate=w["post"], out=a)
+    assert o is a and torch.equal(a, out) and torch.equal(n, normed)
+    b = x.clone()
+    o, n = layer(b, residual=b, gate=w["post"], normed=b)
+    assert n is b and torch.equal(o, out) and torch.equal(b, normed)
+
+
+@pytest.mark.gpu
 def test_same_experts_for_every_token():
     """All tokens alike: each chosen expert has two full tiles, the others none."""
     w = make(24, 256, 192, seed=11)
