@@ -38,20 +38,22 @@ class MoeRouter(ctypes.Structure):
                 ("weight", ctypes.c_void_p), ("expert_scale", ctypes.c_void_p)]
 
 
-_package = None
+# The package, which imports this module, and torch, which it does without until a
+# tensor is there: imported by the first call (_api).  Import statements in the
+# functions cost a call 0.3 us.
+_package = torch = None
 
 
 def _api():
-    """The package (imported late: it imports this module)."""
-    global _package
+    global _package, torch
     if _package is None:
+        import torch as t
         import bit_gathered_quantized_amd as bgq
-        _package = bgq
+        torch, _package = t, bgq
     return _package
 
 
 def _type(t, name):
-    import torch
     if t.dtype is torch.bfloat16:
         return MOE_T_BF16
     if t.dtype is torch.float32:
@@ -92,14 +94,12 @@ def _vector(t, name, dev, n):
 
 def _like(t):
     """A new contiguous tensor of t's shape and type."""
-    import torch
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 @contextlib.contextmanager
 def _ambient(dev, stream):
     """Makes the tensors' device, and the stream if one is given, current."""
-    import torch
     with contextlib.ExitStack() as stack:
         if dev.index != torch.cuda.current_device():
             stack.enter_context(torch.cuda.device(dev))
@@ -112,7 +112,6 @@ def _ambient(dev, stream):
 
 def _call(dev, stream, f):
     """f(raw stream) with the device and stream current; no context in the usual case."""
-    import torch
     if stream is None and dev.index == torch.cuda.current_device():
         return f(torch._C._cuda_getCurrentRawStream(dev.index))  # current_stream() without its object
     with _ambient(dev, stream):
@@ -182,7 +181,6 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None
 
     Returns out, (out, normed) with a norm after the block, or normed alone
     with want_out=False."""
-    import torch
     bgq = _api()
     dev = _device(y, "y")
     if y.dim() != 2:
@@ -238,7 +236,6 @@ def _output(t, name, dev, shape, dtype):
 
 def _new_or_given(t, name, dev, shape, dtype):
     """The output, allocated unless given, and its data pointer."""
-    import torch
     if t is not None:
         return t, _output(t, name, dev, shape, dtype)
     t = torch.empty(shape, dtype=dtype, device=dev)
@@ -257,7 +254,6 @@ def router_forward(x, weight, k, *, norm=True, eps=1e-6, expert_scale=None, logi
     lower id first on ties), weights fp32 [T, k] their softmax, times
     expert_scale[id] if given (fp32 [E]).  Products of x are exact and sums fp32
     whichever type the weight has.  Returns (logits fp32 [T, E], ids, weights)."""
-    import torch
     bgq = _api()
     dev = _device(x, "x")
     if x.dim() != 2 or weight.dim() != 2:
@@ -322,7 +318,6 @@ class MoeLayer:
     def __init__(self, router_weight, k, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, *, norm=True,
                  norm_weight=None, router_norm=True, expert_scale=None, post_norm=False, post_weight=None,
                  pre_norm=False, pre_weight=None, weight_offset=0.0, swiglu=False, fp32_intermediate=False, eps=1e-6):
-        import torch
         bgq = _api()
         dev = self.device = _device(router_weight, "router_weight")
         if router_weight.dim() != 2 or not router_weight.is_contiguous():
@@ -386,7 +381,6 @@ class MoeLayer:
         [T, k], receive the routing if given.  workspace: a uint8 tensor of
         workspace_bytes(T) bytes, one per call at a time (allocated if None).  Returns
         out, or (out, normed) if the layer norms its output."""
-        import torch
         bgq = _api()
         dev, H, k = self.device, self.H, self.k
         if x.dim() != 2 or x.shape[1] != H or x.dtype is not torch.bfloat16 or not x.is_contiguous():
