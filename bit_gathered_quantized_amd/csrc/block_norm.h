@@ -89,8 +89,13 @@ __device__ __forceinline__ void store_values(Rsrc r, int c, const float (&v)[VEC
 // thread: lanes by exchange, waves through LDS in wave order.
 template <int WAVES>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
+    // lanes i ^ 1, i ^ 2, then mirrors of 8 and 16 once quads agree, without LDS
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));
+    v += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
     if constexpr (WAVES > 1) {
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
         __syncthreads();
