@@ -308,7 +308,8 @@ class MoeLayer:
     Weights as for router_forward and expert_ffn_forward; norm_weight, post_weight
     and pre_weight are [H] in bf16 or fp32 (post and pre alike; pre_norm=True or
     post_norm=True without a weight norms by ones).  The handle checks them once and
-    keeps them alive; it holds no other state, so calls on several streams are
+    keeps their memory alive, so a parameter that is moved or converted later needs a
+    new handle; it holds no other state, so calls on several streams are
     independent as long as each has a workspace of its own.
 
     Calls of up to 16 tokens take two launches."""
@@ -360,8 +361,11 @@ class MoeLayer:
         self._pre = _norm_tail(self._tail, 0, H, dev, None, post_norm, post_weight, None, 1.0, pre_norm, pre_weight,
                                weight_offset, eps)
         self._flags = (bgq.MOE_F_SWIGLU if swiglu else 0) | (bgq.MOE_F_FP32_INTERMEDIATE if fp32_intermediate else 0)
-        self._keep = (router_weight, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, norm_weight, expert_scale,
-                      post_weight, pre_weight)
+        # detached: tensors of their own on the same memory.  A module's .to() or an
+        # assignment to .data gives a parameter other memory under the same object.
+        self._keep = tuple(None if t is None else t.detach() for t in (
+            router_weight, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, norm_weight, expert_scale, post_weight,
+            pre_weight))
         if self.workspace_bytes(1) == 0:
             raise ValueError(f"unsupported layer: E={E}, H={H}, I={I}, k={k}, group size {gs}, {bits} bits")
 
