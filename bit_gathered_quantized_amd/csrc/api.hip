@@ -285,7 +285,7 @@ moe_status check_router(const moe_router* r) {
     if (r->E > MOE_MAX_EXPERTS || r->k > moe::kRouterMaxK || r->H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
     if (!(r->eps >= 0.f)) return MOE_ERR_SHAPE;
     if (r->x_stride < r->H || r->x_stride > MOE_ROUTER_MAX_STRIDE) return MOE_ERR_SHAPE;
-    if (static_cast<int64_t>(r->T) * r->E > INT32_MAX) return MOE_ERR_SHAPE;
+    if (static_cast<int64_t>(r->T) * r->E > INT32_MAX || r->T > MOE_ROUTER_MAX_TOKENS) return MOE_ERR_SHAPE;
     if (r->T == 0) return MOE_OK;
     if (!r->weight) return MOE_ERR_NULL;
     if (r->x_stride % 8 || !aligned(r->weight, 16) || !aligned(r->expert_scale, 4)) return MOE_ERR_ALIGN;

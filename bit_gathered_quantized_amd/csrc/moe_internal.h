@@ -195,6 +195,18 @@ inline hipError_t launch_kernel(F kernel, dim3 grid, dim3 block, hipStream_t str
     return launch_kernel_lds(kernel, grid, block, 0, stream, t, args...);
 }
 
+// A dimension of a launch holds fewer than 2^32 threads, and HIP does not refuse more:
+// it starts what is left of their number modulo 2^32.  Up to 2^31 workgroups of at most
+// 1024 threads go to two dimensions, 2^21 to a row.
+constexpr int kGridRowLog = 21;
+inline dim3 grid_of(int64_t workgroups) {
+    const int64_t row = 1 << kGridRowLog;
+    return dim3(static_cast<unsigned>(workgroups < row ? workgroups : row),
+                static_cast<unsigned>((workgroups + row - 1) >> kGridRowLog));
+}
+// This workgroup's number in such a grid; the last row may go past `workgroups`.
+__device__ __forceinline__ uint32_t grid_index() { return blockIdx.x + (blockIdx.y << kGridRowLog); }
+
 struct RouteArgs {
     const int32_t* ids;
     int32_t A, E, bm_big, bm_small, max_tiles;

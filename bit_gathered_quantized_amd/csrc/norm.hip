@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void moe_block_norm_kernel(Nor
     constexpr int kRows = kNormThreads<WAVES> / 64 / WAVES, kStep = 64 * WAVES * VEC;
     __shared__ float lds[2][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kRows + (WAVES == 1 ? wave : 0);
+    const int64_t t = static_cast<int64_t>(grid_index()) * kRows + (WAVES == 1 ? wave : 0);
     if (t >= a.T) return;  // whole waves of one row: no barrier is left waiting
     const int c0 = VEC * (WAVES == 1 ? threadIdx.x & 63 : threadIdx.x);
     Raw<VEC> ry[NV];
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kNormThreads<WAVES>) void moe_block_norm_kernel(Nor
 template <int WAVES, int NV, int VEC, bool kYF32, bool kSF32, bool kSlots = false>
 hipError_t launch_one(const NormArgs& a, hipStream_t s) {
     constexpr int kRows = kNormThreads<WAVES> / 64 / WAVES;
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.T) + kRows - 1) / kRows));
+    const dim3 grid = grid_of((static_cast<int64_t>(a.T) + kRows - 1) / kRows);
     hipLaunchKernelGGL((moe_block_norm_kernel<WAVES, NV, VEC, kYF32, kSF32, kSlots>), grid, dim3(kNormThreads<WAVES>), 0,
                        s, a);
     return hipGetLastError();

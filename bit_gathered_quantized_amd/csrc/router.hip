@@ -20,8 +20,8 @@ __global__ __launch_bounds__(64 * kRouterTokensPerBlock) void moe_router_topk_ke
     const float* __restrict__ logits, int32_t T, int32_t E, int32_t k,
     const float* __restrict__ expert_scale, int32_t* __restrict__ ids, float* __restrict__ weights) {
     const int lane = threadIdx.x & 63;
-    const int t = blockIdx.x * kRouterTokensPerBlock + (threadIdx.x >> 6);
-    if (t >= T) return;  // whole wave; no barrier follows
+    const uint32_t t = grid_index() * kRouterTokensPerBlock + (threadIdx.x >> 6);
+    if (t >= static_cast<uint32_t>(T)) return;  // whole wave; no barrier follows
     const float* row = logits + static_cast<size_t>(t) * E;
     float v[PER];
 #pragma unroll
@@ -37,7 +37,8 @@ __global__ __launch_bounds__(64 * kRouterTokensPerBlock) void moe_router_topk_ke
 
 hipError_t launch_router_topk(const float* logits, int32_t T, int32_t E, int32_t k, const float* expert_scale,
                               int32_t* ids, float* weights, hipStream_t stream) {
-    const dim3 grid((T + kRouterTokensPerBlock - 1) / kRouterTokensPerBlock), block(64 * kRouterTokensPerBlock);
+    const dim3 grid = grid_of((static_cast<int64_t>(T) + kRouterTokensPerBlock - 1) / kRouterTokensPerBlock);
+    const dim3 block(64 * kRouterTokensPerBlock);
     if (E <= 128)
         hipLaunchKernelGGL(moe_router_topk_kernel<2>, grid, block, 0, stream, logits, T, E, k, expert_scale, ids, weights);
     else if (E <= 256)

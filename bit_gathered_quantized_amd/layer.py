@@ -186,6 +186,8 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None
     if y.dim() != 2:
         raise ValueError(f"y has shape {tuple(y.shape)}, expected [T, H]")
     T, H = y.shape
+    if T > 2**31 - 1:
+        raise ValueError(f"y has {T} rows, more than a call takes (2^31 - 1)")
     n = MoeNorm()
     n.y_type = _type(y, "y")
     n.y_stride = _rows(y, "y", dev, T, H)

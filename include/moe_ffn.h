@@ -400,7 +400,7 @@ moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream);
  */
 #define MOE_R_NORM 1u
 typedef struct {
-    int32_t T;                 /* tokens, >= 0                                       */
+    int32_t T;                 /* tokens, 0 <= T <= MOE_ROUTER_MAX_TOKENS, T E < 2^31 */
     int32_t H;                 /* multiple of 64, <= MOE_NORM_MAX_H                  */
     int32_t E;                 /* experts, 1 <= E <= MOE_MAX_EXPERTS                 */
     int32_t k;                 /* experts per token, 1 <= k <= min(E, 64)            */
@@ -413,6 +413,7 @@ typedef struct {
     const float* expert_scale; /* [E] or NULL                                        */
 } moe_router;
 #define MOE_ROUTER_MAX_STRIDE (1 << 22)
+#define MOE_ROUTER_MAX_TOKENS ((1 << 30) - 64) /* 2^24 - 1 workgroups of 64 tokens and 256 threads */
 
 /* x bf16 [T, H], 16-byte aligned; logits fp32 [T, E]; topk_ids int32 [T, k];
  * topk_weights fp32 [T, k].  Deterministic; a token's logits may differ in
