@@ -47,6 +47,17 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Wide tiles of at most 64 rows (4 row blocks per wave), or 32 with an fp32 h (the
+// down matmul carries two activation parts) or 8-bit codes (twice the weight words
+// in flight).
+int32_t big_rows(const moe_problem* p) {
+    return (p->flags & MOE_F_FP32_INTERMEDIATE) || p->bits == 8 ? moe::kBmBigF32 : moe::kBmBig;
+}
+
+// Whether a one-dimensional launch of `groups` workgroups has fewer than 2^32 threads.
+// HIP does not refuse more: it starts what is left of their number modulo 2^32.
+bool fits_launch(int64_t groups, int64_t threads) { return groups * threads < (int64_t{1} << 32); }
+
 // Shape checks shared by the forward's size queries and the forward itself.
 moe_status check_problem(const moe_problem* p) {
     if (!p) return MOE_ERR_NULL;
@@ -65,16 +76,19 @@ moe_status check_problem(const moe_problem* p) {
     if (p->H > moe::kMaxDim || p->I > moe::kMaxDim) return MOE_ERR_UNSUPPORTED;
     const int64_t A = static_cast<int64_t>(p->T) * p->k;
     if (A > INT32_MAX / 2) return MOE_ERR_SHAPE;
+    // the route's launch (x in pieces of 8 columns) and the wide matmuls'
+    const int64_t tiles = moe_max_tiles(A, p->E, big_rows(p)), T = p->T;
+    const int64_t route = moe::route_count_wgs(A) + 1 + (T * (p->H / 8) + moe::kRouteThreads - 1) / moe::kRouteThreads;
+    if (!fits_launch(route, moe::kRouteThreads) || !fits_launch(tiles * ((p->I + 127) / 128) + 7, moe::kWideThreads) ||
+        !fits_launch(tiles * ((p->H + 255) / 256) + 7, moe::kWideThreads))
+        return MOE_ERR_SHAPE;
     return MOE_OK;
 }
 
 moe_ws_layout make_layout(const moe_problem* p) {
     moe_ws_layout l = {};
     const int64_t A = static_cast<int64_t>(p->T) * p->k;
-    // Wide tiles of at most 64 rows (4 row blocks per wave), or 32 with an
-    // fp32 h (the down matmul carries two activation parts) or 8-bit codes
-    // (twice the weight words in flight).
-    l.bm_big = (p->flags & MOE_F_FP32_INTERMEDIATE) || p->bits == 8 ? moe::kBmBigF32 : moe::kBmBig;
+    l.bm_big = big_rows(p);
     l.bm_small = moe::kBmSmall;
     l.max_tiles = moe_max_tiles(A, p->E, l.bm_big);
     l.max_skinny = moe_max_tiles(A, p->E, l.bm_small);
@@ -117,6 +131,9 @@ moe_status forward_impl(const moe_problem* p, const void* x, const int32_t* ids,
                         bool combine = true) {
     const moe_status st = check_problem(p);
     if (st != MOE_OK) return st;
+    if (combine && !fits_launch((static_cast<int64_t>(p->T) * (p->H / 4) + moe::kCombineThreads - 1) / moe::kCombineThreads,
+                                moe::kCombineThreads))
+        return MOE_ERR_SHAPE;
     if (p->T == 0) return MOE_OK;
     if (!x || !ids || !topk_w || !w_gu || !s_gu || !b_gu || !w_d || !s_d || !b_d || (combine && !out))
         return MOE_ERR_NULL;

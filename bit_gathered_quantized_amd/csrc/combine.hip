@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 template <bool kF32Out>
-__global__ __launch_bounds__(256) void moe_combine(FfnArgs a) {
+__global__ __launch_bounds__(kCombineThreads) void moe_combine(FfnArgs a) {
     const int H4 = a.H / 4;
     const size_t idx = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const size_t total = static_cast<size_t>(a.T) * H4;
@@ -55,11 +55,11 @@ __global__ __launch_bounds__(256) void moe_combine(FfnArgs a) {
 
 hipError_t launch_combine(const FfnArgs& a, hipStream_t stream, const KTiming& t) {
     const size_t total = static_cast<size_t>(a.T) * (a.H / 4);
-    const dim3 grid(static_cast<unsigned>((total + 255) / 256));
+    const dim3 grid(static_cast<unsigned>((total + kCombineThreads - 1) / kCombineThreads));
     if (a.flags & MOE_F_FP32_OUT)
-        return launch_kernel(moe_combine<true>, grid, dim3(256), stream, t, a);
+        return launch_kernel(moe_combine<true>, grid, dim3(kCombineThreads), stream, t, a);
     else
-        return launch_kernel(moe_combine<false>, grid, dim3(256), stream, t, a);
+        return launch_kernel(moe_combine<false>, grid, dim3(kCombineThreads), stream, t, a);
 }
 
 }  // namespace moe

@@ -56,7 +56,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kWideThreads;
 // skinny paths (one wave per workgroup): 16-column weight blocks per wave
 // and weight chunks in flight
 constexpr int kSkinnyGateUpRing = 2;

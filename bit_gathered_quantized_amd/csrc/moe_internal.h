@@ -19,6 +19,8 @@ typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kWideThreads = 256;     // of a workgroup of the wide matmuls
+constexpr int kCombineThreads = 256;  // four columns each
 
 // Tile heights used by the forward's own routing: an expert of at most 16
 // rows is one skinny tile; a larger one is cut into ceil(rows / 64) wide

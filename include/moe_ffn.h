@@ -76,7 +76,10 @@ typedef struct {
 
 /* Problem description.  Append-only: new fields go at the end. */
 typedef struct {
-    int32_t T;          /* tokens, >= 0                                  */
+    int32_t T;          /* tokens, >= 0; T * k < 2^30, and no launch of
+                           2^32 threads: T * H < 2^34 with a combine,
+                           T * k * max(I, 128) < 2^37 about, half with
+                           fp32 h or 8-bit codes (else MOE_ERR_SHAPE)    */
     int32_t k;          /* experts per token, 1 <= k <= E                */
     int32_t E;          /* experts, 1 <= E <= MOE_MAX_EXPERTS            */
     int32_t H;          /* hidden size, multiple of 64 and of group_size, <= 4096 */

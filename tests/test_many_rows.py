@@ -46,3 +46,17 @@ def test_topk():
     logits = torch.randn(T, E, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
     ids, weights = bgq.router_topk(logits, 1)
     assert torch.equal(ids[:, 0].long(), logits.argmax(-1)) and bool((weights == 1.0).all())
+
+
+@pytest.mark.parametrize("T,k,H,I,kw,fits", [
+    ((1 << 22) - 1, 1, 4096, 64, {}, True), (1 << 22, 1, 4096, 64, {}, False),        # combine: T H / 4 threads
+    (1 << 24, 8, 64, 4096, {}, False), ((1 << 24) - 64, 1, 64, 4096, {}, True),      # gate|up: tiles of 64 rows by 128 columns
+    ((1 << 24) - 64, 1, 64, 4096, dict(bits=8), False),                              # tiles of 32 rows
+    ((1 << 23) - 1024, 1, 64, 4096, dict(bits=8), True),
+    (1 << 25, 1, 64, 64, dict(flags=2), True), (1 << 29, 1, 64, 64, dict(flags=2), False)])
+def test_expert_ffn_refuses_sizes_past_a_launch(T, k, H, I, kw, fits):
+    """What fits goes on to the next check, that of the workspace."""
+    p = bgq.problem(T, k, 8, H, I, **kw)
+    some = ctypes.c_void_p(0x10000)
+    st = bgq.lib().moe_expert_ffn_forward(ctypes.byref(p), *[some] * 9, some, some, 0, None)
+    assert st == (-5 if fits else -2)
