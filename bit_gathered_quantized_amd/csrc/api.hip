@@ -365,6 +365,13 @@ LayerLayout layer_layout(const moe_problem* p) {
         l.ffn = take(make_layout(p).total);
     }
     l.total = off;
+    if (!l.few) {
+        // never less than a smaller batch takes: the few-token form keeps n and h wider
+        moe_problem most = *p;
+        most.T = MOE_LAYER_FEW_TOKENS;
+        const size_t few = layer_layout(&most).total;
+        if (l.total < few) l.total = few;
+    }
     return l;
 }
 

@@ -375,7 +375,7 @@ class MoeLayer:
         return _api().problem(T, self.k, self.E, self.H, self.I, self._flags, group_size=self.group_size, bits=self.bits)
 
     def workspace_bytes(self, T):
-        """Bytes of device workspace a call on T tokens needs (0: unsupported)."""
+        """Bytes of device workspace a call on T tokens, or fewer, needs (0: unsupported)."""
         return int(_api().lib().moe_layer_workspace_bytes(ctypes.byref(self._problem(T))))
 
     def __call__(self, x, *, residual=None, gate=None, residual_scale=1.0, out=None, normed=None, ids=None, weights=None,

@@ -461,7 +461,8 @@ typedef struct {
     float* topk_weights;       /* out: fp32 [T, k], or NULL                          */
 } moe_layer;
 
-/* Device workspace of moe_layer_forward (0 on an invalid p). */
+/* Device workspace of moe_layer_forward (0 on an invalid p): one for the largest T
+ * of a program serves every smaller one. */
 size_t moe_layer_workspace_bytes(const moe_problem* p);
 
 /* p as for moe_expert_ffn_forward, without MOE_F_FP32_OUT and with k <= 64; x bf16

@@ -80,3 +80,11 @@ def test_calls_after_the_parameters_moved():
     junk = [torch.full((s,), 0x7F, dtype=torch.uint8, device="cuda") for s in sizes.values() for _ in range(3)]
     got = layer(x, residual=x)
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 3 * len(sizes)
+
+
+@pytest.mark.parametrize("kw", [{}, dict(bits=8), dict(flags=2), dict(group_size=32, flags=4)])
+@pytest.mark.parametrize("E_,H_,I_,k", [(128, 2816, 704, 8), (8, 256, 128, 2), (64, 64, 1024, 16)])
+def test_workspace_of_a_batch_serves_every_smaller_one(E_, H_, I_, k, kw):
+    """A program sizes one workspace for its largest batch."""
+    sizes = [bgq.lib().moe_layer_workspace_bytes(ctypes.byref(bgq.problem(T, k, E_, H_, I_, **kw))) for T in range(1, 80)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
