@@ -363,6 +363,11 @@ class MoeLayer:
         self._pre = _norm_tail(self._tail, 0, H, dev, None, post_norm, post_weight, None, 1.0, pre_norm, pre_weight,
                                weight_offset, eps)
         self._flags = (bgq.MOE_F_SWIGLU if swiglu else 0) | (bgq.MOE_F_FP32_INTERMEDIATE if fp32_intermediate else 0)
+        for desc, names in ((d, ("router_weight", "norm_weight", "w_gateup", "s_gateup", "b_gateup", "w_down", "s_down",
+                                 "b_down")), (self._tail, ("post_weight", "pre_weight"))):
+            for name in names:
+                if (getattr(desc, name) or 0) % 16:
+                    raise ValueError(f"{name} must start on 16 bytes")
         # detached: tensors of their own on the same memory.  A module's .to() or an
         # assignment to .data gives a parameter other memory under the same object.
         self._keep = tuple(None if t is None else t.detach() for t in (

@@ -88,3 +88,20 @@ def test_workspace_of_a_batch_serves_every_smaller_one(E_, H_, I_, k, kw):
     """A program sizes one workspace for its largest batch."""
     sizes = [bgq.lib().moe_layer_workspace_bytes(ctypes.byref(bgq.problem(T, k, E_, H_, I_, **kw))) for T in range(1, 80)]
     assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+ALL = FLOATS + ("w_gateup", "s_gateup", "b_gateup", "w_down", "s_down", "b_down")
+
+
+@pytest.mark.parametrize("name", [n for n in ALL if n != "expert_scale"])
+def test_refuses_weights_off_16_bytes(on_cpu, name):
+    """When the handle is made, by name: a call would refuse them too."""
+    w = weights()
+    t = w[name]
+    flat = torch.empty(t.numel() + 16, dtype=t.dtype)
+    w[name] = flat[4:4 + t.numel()].view(t.shape)  # 8 or 16 bytes on
+    if t.element_size() == 4:
+        w[name] = flat[2:2 + t.numel()].view(t.shape)
+    assert w[name].data_ptr() % 16 == 8
+    with pytest.raises(ValueError, match=f"{name} must start on 16 bytes"):
+        make(w)
