@@ -105,3 +105,20 @@ def test_refuses_weights_off_16_bytes(on_cpu, name):
     assert w[name].data_ptr() % 16 == 8
     with pytest.raises(ValueError, match=f"{name} must start on 16 bytes"):
         make(w)
+
+
+@pytest.mark.parametrize("name,dtype", [("s_gateup", torch.float16), ("b_down", torch.float16), ("w_gateup", torch.float32),
+                                        ("w_down", torch.float32)])
+def test_refuses_types_that_hold_no_codes_or_bf16(on_cpu, name, dtype):
+    """float16 scales would be read as bf16 bits, and float weights as codes."""
+    w = weights()
+    w[name] = w[name].to(dtype)
+    with pytest.raises(ValueError, match=f"{name} must"):
+        make(w)
+
+
+def test_takes_integers_that_hold_bf16_bits(on_cpu):
+    w = weights()
+    for n in ("s_gateup", "b_gateup", "s_down", "b_down"):
+        w[n] = w[n].view(torch.int16)
+    make(w)
