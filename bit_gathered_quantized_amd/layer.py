@@ -344,9 +344,8 @@ class MoeLayer:
                                      ("w_down", w_down, 4, (E, H, I * bits // 32)),
                                      ("s_down", s_down, 2, (E, H, I // gs)), ("b_down", b_down, 2, (E, H, I // gs))):
             _on(t, name, dev)
-            if t.is_floating_point() and (size == 4 or t.dtype is not torch.bfloat16):
-                raise ValueError(f"{name} must hold " + ("codes in 4-byte integers" if size == 4 else
-                                                         "bfloat16 values (or their bits in integers)") + f", got {t.dtype}")
+            if t.dtype is torch.float16:
+                raise ValueError(f"{name} must hold bfloat16 values (or their bits in 2-byte integers), got {t.dtype}")
             setattr(d, name, bgq._dev_ptr(t, name, size, shape).value)
         d.flags = 1 if norm else 0
         d.router_flags = MOE_R_NORM if router_norm else 0
