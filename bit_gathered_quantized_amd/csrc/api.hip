@@ -242,8 +242,14 @@ moe_status forward_impl(const moe_problem* p, const void* x, const int32_t* ids,
 bool known_type(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP32; }
 size_t type_size(int32_t t) { return t == MOE_T_FP32 ? 4 : 2; }
 
-// The checks of a block norm apart from y's pointer (y_stride is checked).
-moe_status check_norm(const moe_norm* n) {
+// Whether an output lies on an input's address without being its very rows.
+bool clashes(const void* out, int32_t type, int64_t stride, const void* in, int32_t in_type, int64_t in_stride, int32_t T) {
+    return out && out == in && (type != in_type || (T > 1 && stride != in_stride));
+}
+
+// The checks of a block norm of y (nullptr: not an address of the caller's), whose
+// pointer itself is left to do.
+moe_status check_norm(const moe_norm* n, const void* y) {
     if (!n) return MOE_ERR_NULL;
     if (!known_type(n->y_type) || !known_type(n->stream_type) || !known_type(n->normed_type) ||
         !known_type(n->weight_type) || !known_type(n->gate_type) || (n->flags & ~MOE_N_POST))
@@ -257,6 +263,12 @@ moe_status check_norm(const moe_norm* n) {
         (n->normed && n->normed_stride < n->H))
         return MOE_ERR_SHAPE;
     if (n->gate && (n->gate_stride_t < 0 || n->gate_stride_h < 0 || n->gate_stride_h > 1)) return MOE_ERR_SHAPE;
+    if ((n->out && n->out == n->normed) ||
+        clashes(n->out, n->stream_type, n->out_stride, y, n->y_type, n->y_stride, n->T) ||
+        clashes(n->out, n->stream_type, n->out_stride, n->residual, n->stream_type, n->residual_stride, n->T) ||
+        clashes(n->normed, n->normed_type, n->normed_stride, y, n->y_type, n->y_stride, n->T) ||
+        clashes(n->normed, n->normed_type, n->normed_stride, n->residual, n->stream_type, n->residual_stride, n->T))
+        return MOE_ERR_UNSUPPORTED;
     const size_t ws = type_size(n->weight_type), ss = type_size(n->stream_type);
     if (!aligned(n->residual, ss) || !aligned(n->out, ss) || !aligned(n->normed, type_size(n->normed_type)) ||
         !aligned(n->post_weight, ws) || !aligned(n->pre_weight, ws) || !aligned(n->gate, type_size(n->gate_type)))
@@ -416,7 +428,7 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
     t.y_type = MOE_T_FP32;
     t.y_stride = p->H;
     if (t.T != p->T || t.H != p->H) return MOE_ERR_SHAPE;
-    if ((st = check_norm(&t)) != MOE_OK) return st;
+    if ((st = check_norm(&t, nullptr)) != MOE_OK) return st;
     if (p->T == 0) return MOE_OK;
     if (!x || !l->w_gateup || !l->s_gateup || !l->b_gateup || !l->w_down || !l->s_down || !l->b_down) return MOE_ERR_NULL;
     if (!aligned(x, 16) || !aligned(l->norm_weight, 16) || !aligned(l->w_gateup, 16) || !aligned(l->s_gateup, 16) ||
@@ -525,7 +537,7 @@ moe_status moe_router_forward(const moe_router* r, const void* x, float* logits,
 }
 
 moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream) {
-    const moe_status st = check_norm(n);
+    const moe_status st = check_norm(n, y);
     if (st != MOE_OK) return st;
     if (n->T == 0) return MOE_OK;
     if (!y) return MOE_ERR_NULL;

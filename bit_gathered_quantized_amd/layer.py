@@ -176,8 +176,8 @@ def block_norm(y, residual=None, *, post_norm=False, post_weight=None, gate=None
     weights alike); rows may be strided.  gate is a number or a tensor that
     broadcasts to [T, H] ([H], [T, 1], ...); weights are [H], None for ones.
     `out` and `normed` are allocated in the residual's type (y's without one)
-    unless given, and may be y or residual themselves.  want_out=False skips
-    `out`: a plain norm of y.
+    unless given, and may be y or residual themselves (but not the same one).
+    want_out=False skips `out`: a plain norm of y.
 
     Returns out, (out, normed) with a norm after the block, or normed alone
     with want_out=False."""

@@ -386,7 +386,8 @@ typedef struct {
 /* Rows are contiguous along H.  Pointers need the alignment of their element;
  * rows that start on 16 bytes with H a multiple of 8 move as 16-byte loads.
  * out and normed must not overlap each other or an input, except that either
- * may be exactly y or residual (same address, type and row stride). */
+ * may be exactly y or residual (same address, type and row stride; the same
+ * address otherwise is MOE_ERR_UNSUPPORTED). */
 moe_status moe_block_norm(const moe_norm* n, const void* y, void* stream);
 
 /*
