@@ -6,6 +6,7 @@
 
 #include <mutex>
 
+#include "layer_cut.h"
 #include "moe_internal.h"
 
 // The built-in workspace of moe_expert_ffn_forward_noalloc: one copy per
@@ -458,10 +459,8 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
         a.norm_f32 = l->norm_type == MOE_T_FP32;
         a.eps = l->eps;
         a.weight_offset = l->weight_offset;
-        const uint32_t upt_gateup = p->I / 16;
-        const uint32_t upt_down = p->H / 32;
-        a.magic_gateup = ((1u << 31) + upt_gateup - 1) / upt_gateup;
-        a.magic_down = ((1u << 31) + upt_down - 1) / upt_down;
+        a.magic_gateup = moe::cut::unit_magic(moe::cut::units_of_tile(false, p->H, p->I));
+        a.magic_down = moe::cut::unit_magic(moe::cut::units_of_tile(true, p->H, p->I));
         a.router = router_args(&r, x, logits);
         a.expert_scale = l->expert_scale;
         a.x = static_cast<const uint16_t*>(x);

@@ -57,15 +57,20 @@
 // needed.
 #include "block_norm.h"
 #include "gemm_kernels.h"
+#include "layer_cut.h"
 #include "router_few.h"
 #include "topk.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8, kFewThreads = 64 * kWaves;
-constexpr int kRanges = kLayerRanges;
-constexpr int kTileRows = 8;
+using cut::kDepth;
+using cut::kLag;
+using cut::kRanges;
+using cut::kTileRows;
+using cut::kWaves;
+constexpr int kFewThreads = 64 * kWaves;
+static_assert(kRanges == kLayerRanges, "ranges");
 constexpr int kMaxSlots = kLayerFewTokens * kRouterMaxK;  // assignments, and so tiles
 constexpr int kSc1 = 16;                                  // buffer access past the XCD's L2
 constexpr int kPad = kLayerCounterStride;                 // counters lie on cache lines of their own
@@ -163,16 +168,8 @@ struct Lists {
 template <int BITS>
 constexpr int kBuffers = BITS == 4 ? 4 : 2;
 
-// The table row of a wave's slice (at most 512 columns): pieces of 16 bytes, from the
-// piece in which the slice begins on.
 template <int GS>
-constexpr int kTablePieces = 512 / GS <= 8 ? 2 : 4;
-
-// Places for the shares of a unit's waves, and units after which its outputs are made.
-constexpr int kDepth = 4, kLag = 2;
-
-// A row of nch chunks is cut over 1 << split_log waves, 4 chunks to a wave at most.
-__device__ __forceinline__ int split_log(int nch) { return nch <= 3 ? 0 : nch <= 6 ? 1 : nch <= 12 ? 2 : 3; }
+constexpr int kTablePieces = cut::table_pieces(GS);
 
 template <int GS, int BITS>
 struct alignas(16) FewSmem {
@@ -403,30 +400,28 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int q = lane >> 4, lr = lane & 15;
     const int K = kDown ? a.I : a.H, G = K / GS, row_words = K / 32 * BITS;
-    const int rows_e = kDown ? a.H : 2 * a.I;     // weight rows of an expert
-    const int upt = kDown ? a.H / 32 : a.I / 16;  // units of a tile
-    const int nch = (K + 127) / 128;
-    const int log_split = split_log(nch), split = 1 << log_split;
+    const int rows_e = cut::expert_rows(kDown, a.H, a.I);
+    const int upt = cut::units_of_tile(kDown, a.H, a.I);
+    const int nch = cut::chunks(K);
+    const int log_split = cut::split_log(nch), split = 1 << log_split;
     const int nu = kWaves >> log_split;           // units at work at a time
     const int wu = wave >> log_split, ws = wave & (split - 1);
-    const int ch0 = nch * ws >> log_split, nc = (nch * (ws + 1) >> log_split) - ch0;  // this wave's chunks, <= CPW
-    const int N = uniform(sm.l.tiles) * upt, shift = 8 + 3 - log_split;  // kRanges * nu shares, N share < 2^30
-    static_assert(kRanges == 1 << 8 && kWaves == 1 << 3, "shift");
-    auto first = [&](int share) { return N * share >> shift; };
+    const int ch0 = cut::first_chunk(nch, log_split, ws), nc = cut::first_chunk(nch, log_split, ws + 1) - ch0;  // <= CPW
+    const int N = uniform(sm.l.tiles) * upt;
+    static_assert(kWaves == 1 << 3, "shares");
+    auto first = [&](int share) { return cut::first_unit(N, share, 3 - log_split); };
     const int r0 = range * nu, lo = first(r0), hi = first(r0 + nu);
     const int u0 = first(r0 + wu), u1 = first(r0 + wu + 1);
-    // u / upt for u < 2^18, upt <= 256, by m = ceil(2^31 / upt): u (m upt - 2^31) < 2^26,
-    // so the quotient errs by less than 1 / upt
     const uint32_t magic = kDown ? a.magic_down : a.magic_gateup;
-    auto tile_of = [&](int u) { return static_cast<int>(__umulhi(2u * u, magic)); };
-    const int block_rows = kDown ? 16 : a.I;  // from its first block of 16 rows to its second
-    const int g0 = ch0 * 128 / GS, ng = min(nc * 128 / GS, G - g0);  // the slice's groups
-    const int cols = min(nc * 128, K - 128 * ch0);                   // and columns
+    auto tile_of = [&](int u) { return cut::tile_of_unit(u, magic); };
+    const int block_rows = cut::block_rows(kDown, a.I);
+    const int g0 = cut::slice_group(GS, ch0), ng = cut::slice_groups(GS, G, ch0, nc);
+    const int cols = cut::slice_columns(K, ch0, nc);
     // The tables' rows of a slice: lane (block, row, piece) loads pieces of 16 bytes.
     // Where the slice begins in its first piece is the same for all units (16 rows are
     // a multiple of 16 bytes).
     const int tb_ = lane >> 5, tr_ = lane >> 1 & 15, tp_ = lane & 1;
-    const uint32_t tat = (2u * (tr_ * G + g0) & ~15u) + 2u * G * block_rows * tb_ + 16 * tp_;
+    const uint32_t tat = cut::table_load(G, g0, block_rows, tb_, tr_, tp_);
     WaveW<2, GS, BITS> ww;
     Rsrc rts, rtb;
     // loads are of unit u from now on, or of nothing from u1 on
@@ -435,7 +430,7 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     auto aim = [&](int u) {
         const bool some = u < u1;
         // its first weight row
-        const uint32_t r = uniform(ahead >> 4) * rows_e + (kDown ? 32 : 16) * (u - tile_of(u) * upt);
+        const uint32_t r = cut::unit_row(kDown, rows_e, uniform(ahead >> 4), u - tile_of(u) * upt);
         const uint32_t* const w = (kDown ? a.w_d : a.w_gu) + static_cast<size_t>(r) * row_words;
         const uint32_t* const blk[2] = {w, w + static_cast<size_t>(block_rows) * row_words};
         ww.init(sm.w[wave][0], blk, row_words);
@@ -509,7 +504,7 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
         }
     };
     // eight entries of a table row of the slice, those past the slice as zeros
-    const int tsub = 2 * (lr * G + g0) & 15;
+    const int tsub = cut::table_start(G, g0, lr);
     auto table8 = [&](int t, int b, int st, int ng) {
         u32x4 v;
         __builtin_memcpy(&v, reinterpret_cast<const char*>(sm.tables[wave][t][b][lr]) + tsub + 16 * st, 16);
@@ -713,8 +708,7 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
 // The same with the chunks of a wave's slice known: up to 2, 3 or 4.
 template <int GS, int BITS, bool kDown>
 __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>& sm, int range, const int32_t* flags) {
-    const int nch = ((kDown ? a.I : a.H) + 127) / 128;
-    const int log_split = split_log(nch), most = (nch + (1 << log_split) - 1) >> log_split;
+    const int most = cut::most_chunks(cut::chunks(kDown ? a.I : a.H));
     if (most <= 2) return run_range<GS, BITS, kDown, 2>(a, sm, range, flags);
     return most <= 3 ? run_range<GS, BITS, kDown, 3>(a, sm, range, flags)
                      : run_range<GS, BITS, kDown, 4>(a, sm, range, flags);
