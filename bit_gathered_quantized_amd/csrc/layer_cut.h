@@ -31,6 +31,9 @@ constexpr int table_pieces(int gs) { return kMaxChunks * kChunk / gs <= 8 ? 2 : 
 // Chunks of a row of K columns.
 MOE_CUT int chunks(int K) { return (K + kChunk - 1) / kChunk; }
 // A row of nch chunks is cut over 1 << split_log waves, kMaxChunks chunks to a wave at most.
+// Measured at rows of 6 and 22 chunks (widths 704, 768 and 2816), which get 3 chunks a
+// wave, against 2; rows of 4, 7, 8 and 13 to 16 chunks get 2, where 4 on half the waves
+// would fit too and has not been measured.
 MOE_CUT int split_log(int nch) { return nch <= 3 ? 0 : nch <= 6 ? 1 : nch <= 12 ? 2 : 3; }
 // The first chunk of wave ws of those waves (ws may be their number).
 MOE_CUT int first_chunk(int nch, int log, int ws) { return nch * ws >> log; }

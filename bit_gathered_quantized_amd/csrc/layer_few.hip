@@ -47,8 +47,8 @@
 // token t's output at last, for those of the token's tiles.  So whoever waits waits
 // for running workgroups, for ranges of an earlier phase than its own, and the first
 // phase waits for nobody: every wait ends, however few workgroups the GPU holds at
-// once.  (Waits are also bounded: a workspace that another call writes to gives NaN,
-// not a hang.)
+// once.  (Waits are also bounded: calls that overlap on one workspace give undefined
+// values, but no hang.)
 //
 // What one workgroup writes and another reads within the launch (h and its sums,
 // y) is stored and loaded past the L2 of the XCD (sc1), rows of whole 128-byte
@@ -74,7 +74,7 @@ static_assert(kRanges == kLayerRanges, "ranges");
 constexpr int kMaxSlots = kLayerFewTokens * kRouterMaxK;  // assignments, and so tiles
 constexpr int kSc1 = 16;                                  // buffer access past the XCD's L2
 constexpr int kPad = kLayerCounterStride;                 // counters lie on cache lines of their own
-constexpr int kSpinLimit = 1 << 22;                       // polls of about 1 us
+constexpr int kSpinLimit = 1 << 22;                       // polls: of memory about 1 us each, of LDS about 0.1 us
 
 // ------------------------------------------------------------ first launch
 template <int TM>
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool wait_lds(const int32_t* p, int32_t want) {
     return ok;
 }
 
-// A wait ran out: every token becomes NaN.
+// A wait ran out: the tokens that are finished after this become NaN.
 __device__ __forceinline__ void give_up(const LayerArgs& a) {
     __hip_atomic_store(a.failed, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -529,7 +529,7 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
     // back.
     const bool idle = u0 == u1;
     int tile_now = idle ? -1 : tile_of(u0);
-    if (tid < kDepth * kWaves) sm.arrived[0][tid] = sm.finished[0][tid] = 0;
+    if (tid < kDepth * kWaves) sm.arrived[tid / kWaves][tid % kWaves] = sm.finished[tid / kWaves][tid % kWaves] = 0;
     if (!idle) {
         look(u0);
         aim(u0);
@@ -540,7 +540,7 @@ __device__ __forceinline__ bool run_range(const LayerArgs& a, FewSmem<GS, BITS>&
         if constexpr (!kDown) split_sums();
     }
     if constexpr (kDown) {
-        const int t = tile_of(lo) + lane;  // at most 4 tiles
+        const int t = tile_of(lo) + lane;  // at most 5 tiles
         if (wave == 0 && lo < hi && t * upt < hi)
             if (!wait_for(a.done_gateup + t * kPad, a.I / 16)) give_up(a);
         __syncthreads();

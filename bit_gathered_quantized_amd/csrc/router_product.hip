@@ -61,7 +61,8 @@ __device__ __forceinline__ void split3(u32x4 a, u32x4 b, u32x4 (&p)[3]) {
 // MT row blocks of 16 tokens, NT of 16 experts, WAVES cuts of the columns.  A wave has
 // the operands of one step of 32 columns in flight: the other waves fill the time, and
 // more steps measured slower (16 x 16 with fp32 weights at 512 tokens, 1 | 2 steps 10.6
-// | 11.3 us; 32 x 32 at 2048, 1 | 2 | 3 steps 16.9 | 18.1 | 19.5 us).
+// | 11.3 us; 32 x 32 at 2048, 1 | 2 | 3 steps 16.9 | 18.1 | 19.5 us; not measured for
+// 64 x 64, whose loads outlast a wave's own MFMAs of a step).
 template <int MT, int NT, int WAVES, bool kWF32>
 __global__ __launch_bounds__(64 * WAVES) void moe_router_product_tile(RouterArgs a) {
     constexpr int kRows = 16 * MT, kExperts = 16 * NT, kW = kWF32 ? 4 : 2, kRaw = kWF32 ? 2 : 1, kParts = kWF32 ? 3 : 1;

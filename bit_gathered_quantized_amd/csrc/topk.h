@@ -91,7 +91,8 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
 }
 
-// The same for E <= 128 and k <= 16, without the factors (8 of 128: 1 us less).  A
+// The same for E <= 128 and k <= 16, without the factors, in the few-token layer (8 of
+// 128: 1 us less there; the router's own launch has not been measured with it).  A
 // lane's two logits lie in order, as keys that order like the floats and leave 0 for
 // "none", so a round looks at one value a lane.  Bit for bit the same.
 __device__ __forceinline__ TopK wave_topk_128(float v0, float v1, int E, int k) {

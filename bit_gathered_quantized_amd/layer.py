@@ -314,9 +314,10 @@ class MoeLayer:
     new handle; it holds no other state, so calls on several streams are
     independent as long as each has a workspace of its own.
 
-    Calls of up to 16 tokens take two launches."""
-
-    FEW_TOKENS = 16
+    Calls of up to 16 tokens take two launches and keep n and h to 16 significant
+    bits.  Larger ones run the operators in turn, with n in bf16 and h in bf16, or in
+    fp32 with fp32_intermediate.  So a token's output differs within these roundings
+    with the size of its batch."""
 
     def __init__(self, router_weight, k, w_gateup, s_gateup, b_gateup, w_down, s_down, b_down, *, norm=True,
                  norm_weight=None, router_norm=True, expert_scale=None, post_norm=False, post_weight=None,

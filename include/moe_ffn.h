@@ -471,7 +471,8 @@ size_t moe_layer_workspace_bytes(const moe_problem* p);
  * used; every row of its tensors starts on 16 bytes; out may be x or the residual
  * itself (same type and row stride).  ws: moe_layer_workspace_bytes(p) bytes,
  * 256-byte aligned, with any contents; one call at a time may use it (calls, or
- * captured graphs, that share one must be ordered by the caller). */
+ * captured graphs, that share one must be ordered by the caller: where two overlap
+ * the outputs of both are undefined). */
 moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const void* x, const moe_norm* tail,
                              void* ws, size_t ws_bytes, void* stream);
 
