@@ -120,8 +120,8 @@ def _call(dev, stream, f):
 
 def _gate(n, gate, dev, T, H):
     """Fills a MoeNorm's gate from a number or a tensor that broadcasts to [T, H]."""
-    if isinstance(gate, (int, float)):
-        n.gate_scale = gate
+    if not hasattr(gate, "data_ptr"):  # a number of any type
+        n.gate_scale = float(gate)
         return
     _on(gate, "gate", dev)
     n.gate_type = _type(gate, "gate")

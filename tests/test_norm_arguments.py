@@ -1,10 +1,14 @@
-"""Tensors of a block norm that lie on one another: exactly the same rows are
-written in place, the same address in any other way is refused."""
+"""Arguments of a block norm: tensors that lie on one another (exactly the same rows
+are written in place, the same address in any other way is refused) and gates that are
+numbers."""
 import ctypes
 
+import numpy as np
 import pytest
+import torch
 
 import bit_gathered_quantized_amd as bgq
+from bit_gathered_quantized_amd import layer as layer_module
 from bit_gathered_quantized_amd.layer import MoeLayerDesc, MoeNorm
 
 Y, RES, OUT, NORMED = 0x10000, 0x20000, 0x30000, 0x40000
@@ -48,3 +52,15 @@ def test_block_norm_takes_the_same_rows(kw):
     n = norm(**kw)
     n.gate, n.gate_type = 0x50002, 1
     assert bgq.lib().moe_block_norm(ctypes.byref(n), Y, None) == -4
+
+
+@pytest.mark.parametrize("gate", [0.5, 2, np.float32(0.25), np.float64(0.125), np.int64(3), True])
+def test_a_gate_may_be_any_number(gate):
+    n = MoeNorm(gate_scale=1.0)
+    layer_module._gate(n, gate, torch.device("cpu"), 4, 64)
+    assert n.gate_scale == float(gate) and not n.gate
+
+
+def test_a_gate_must_be_a_number_or_a_tensor():
+    with pytest.raises((TypeError, ValueError)):
+        layer_module._gate(MoeNorm(), "wide", torch.device("cpu"), 4, 64)
