@@ -110,3 +110,100 @@ def test_one_workspace_for_every_batch():
     for T in (17, 16, 3, 1, 17):
         x = base.tokens(w, T)
         assert all(torch.equal(a, b) for a, b in zip(layer(x, residual=x, workspace=ws), layer(x, residual=x)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 40])
+@pytest.mark.parametrize("gs,bits", [(64, 4), (32, 4), (64, 8)])
+def test_bad_tokens_stay_by_themselves(T, gs, bits):
+    """A NaN or an infinity makes its own token NaN and no other; the others are those
+    of the batch with harmless tokens in their places, up to the roundings that go by an
+    expert's number of rows (2^-9 of n, of h and of the output, and those of the block
+    scales' operands: as a whole 4 of them)."""
+    w = base.make(12, 640, 192, gs=gs, bits=bits, seed=24)
+    layer = base.layer_of(w, 3, norm_weight=w["norm"], **tail_args(w))
+    good = base.tokens(w, T)
+    x = good.clone()
+    x[1, 3], x[2, 600], x[3] = float("nan"), float("inf"), 0
+    ids = torch.empty(T, 3, dtype=torch.int32, device="cuda")
+    out, normed = layer(x, ids=ids)
+    want, want_normed = layer(good)
+    assert bool(((ids >= 0) & (ids < 12)).all())
+    for got, ref in ((out, want), (normed, want_normed)):
+        assert bool(torch.isnan(got[1:3]).all()) and bool((got[3] == 0).all())
+        rest = [0] + list(range(4, T))
+        a, b = got[rest].double(), ref[rest].double()
+        assert bool(torch.isfinite(a).all())
+        assert float(torch.linalg.norm(a - b) / torch.linalg.norm(b)) <= 4 * 2.0 ** -9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [333, 1001, 16383])
+def test_norm_of_bad_rows_off_16_bytes(H):
+    g = torch.Generator(device="cuda").manual_seed(H)
+    y = torch.randn(6, H, generator=g, device="cuda").bfloat16()
+    res = torch.randn(6, H, generator=g, device="cuda").bfloat16()
+    want, want_normed = bgq.block_norm(y, res, post_norm=True, pre_norm=True)
+    y2 = y.clone()
+    y2[2, H - 1], y2[4, 0] = float("nan"), float("inf")
+    out, normed = bgq.block_norm(y2, res, post_norm=True, pre_norm=True)
+    keep = [0, 1, 3, 5]
+    assert torch.equal(out[keep], want[keep]) and torch.equal(normed[keep], want_normed[keep])
+    assert bool(torch.isnan(out[2]).all()) and bool(torch.isnan(normed[2]).all()) and bool(torch.isnan(normed[4]).all())
+    # an infinity's mean of squares is infinite: the rest of its row is 0 before the residual
+    assert torch.isnan(out[4, 0]) and torch.equal(out[4, 1:], res[4, 1:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [7, 40])
+def test_two_graphs_of_two_layers_at_once(T):
+    """Two handles, captured with what they allocate, replayed together on two streams."""
+    ws = [base.make(16, 512, 256, seed=s) for s in (25, 26)]
+    layers = [base.layer_of(w, 4, norm_weight=w["norm"], **tail_args(w)) for w in ws]
+    xs = [base.tokens(w, T) for w in ws]
+    for layer, x in zip(layers, xs):
+        layer(x, residual=x)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for layer, x in zip(layers, xs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(layer(x, residual=x))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for rep in range(3):
+        for w, x in zip(ws, xs):
+            x.copy_(base.tokens(w, T))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for layer, x, got in zip(layers, xs, outs):
+            assert all(torch.equal(a, b) for a, b in zip(got, layer(x, residual=x))), rep
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 20])
+def test_weights_past_32_bit_offsets(T):
+    """6.7 GB of gate|up codes: most experts lie past 2^32 bytes."""
+    E, H, I, k = 200, 4096, 4096, 4
+    if T <= 16:
+        _, w, layer, x = base.run_case(T, E, H, I, k, bits=8, seed=27)
+    else:
+        w = base.make(E, H, I, bits=8, seed=27)
+        layer, x = base.layer_of(w, k, norm_weight=w["norm"]), base.tokens(w, T)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    out = layer(x, ids=ids, out=torch.empty(T, H, device="cuda"))
+    far = ids.amax(1) * (2 * I * H) > 2**32
+    assert bool(far.any())
+    # the same token by a layer of its experts alone, in the order of their logits
+    t = int(far.nonzero()[0])
+    own = ids[t].long()
+    small = dict(w, **{n: w[n][own].contiguous() for n in w if n[:2] in ("w_", "s_", "b_")}, router=w["router"][own].contiguous())
+    got = base.layer_of(small, k, norm_weight=w["norm"], expert_scale=w["expert_scale"][own] if T <= 16 else None)(
+        x[t:t + 1].contiguous(), out=torch.empty(1, H, device="cuda"))[0].double()
+    want = out[t].double()
+    # the order of the sums over experts, and n and h in bf16 in the larger batch
+    assert float(torch.linalg.norm(got - want) / torch.linalg.norm(want)) <= (1e-5 if T <= 16 else 3 * 2.0 ** -9)

@@ -69,3 +69,18 @@ def test_values(wt, T, E, H, tile, xcd):
     assert bool((err <= bound).all())
     assert rel <= U * math.sqrt(L)  # signs as good as random
     assert torch.equal(ids.long(), logits.sort(dim=-1, descending=True, stable=True).indices[:, :k])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [8, 2100])
+def test_rows_past_32_bit_offsets(T):
+    """Rows 2^22 (8 tokens: the widest there is) or 2^20 elements apart."""
+    H, stride = 320, 1 << (22 if T == 8 else 20)
+    rows = 600 if T == 8 else T
+    big = torch.zeros(rows, stride, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(T, H, device="cuda").bfloat16()
+    view = big[rows - T:, stride - H:]
+    view.copy_(x)
+    w = torch.randn(40, H, device="cuda").bfloat16()
+    for a, b in zip(bgq.router_forward(view, w, 3), bgq.router_forward(x, w, 3)):
+        assert torch.equal(a, b)
