@@ -207,3 +207,26 @@ def test_weights_past_32_bit_offsets(T):
     want = out[t].double()
     # the order of the sums over experts, and n and h in bf16 in the larger batch
     assert float(torch.linalg.norm(got - want) / torch.linalg.norm(want)) <= (1e-5 if T <= 16 else 3 * 2.0 ** -9)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 12])
+def test_same_bits_beside_other_work(T):
+    """Workgroups that start late, because other streams hold the GPU, leave their ranges
+    to others: the bits stay."""
+    w = base.make(32, 704, 320, seed=28)
+    layer = base.layer_of(w, 6, norm_weight=w["norm"], **tail_args(w))
+    x, other = base.tokens(w, T), base.tokens(w, T)
+    want = layer(x, residual=x)
+    a = torch.randn(2048, 2048, device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(60):
+        for s in streams:
+            with torch.cuda.stream(s):
+                _ = (a @ a).sum()
+        if i % 3 == 0:
+            layer(other, residual=other)
+        got = layer(x, residual=x)
+        assert all(torch.equal(u, v) for u, v in zip(got, want)), i
+    torch.cuda.synchronize()
