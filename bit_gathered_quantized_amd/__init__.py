@@ -11,13 +11,16 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
+from .grouped import (MoeGrouped, MoeGroupedGrad, MoeMx, grouped_dw_workspace_bytes, grouped_matmul, grouped_matmul_dw,
+                      mx_dequantize, mx_quantize)
 from .layer import MoeLayer, MoeLayerDesc, MoeNorm, MoeRouter, block_norm, router_forward
 
 __all__ = [
     "MoeError", "lib", "LIB_PATH", "MOE_F_FP32_OUT", "MOE_F_FP32_INTERMEDIATE", "MOE_F_SWIGLU",
     "max_tiles", "workspace_bytes", "workspace_layout", "sort_build_tiles",
     "expert_ffn_forward", "router_topk", "status_string", "EXPORTED_SYMBOLS",
-    "block_norm", "router_forward", "MoeLayer",
+    "block_norm", "router_forward", "MoeLayer", "grouped_matmul", "grouped_matmul_dw", "grouped_dw_workspace_bytes",
+    "mx_quantize", "mx_dequantize",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoeffn.so")
@@ -37,7 +40,8 @@ EXPORTED_SYMBOLS = (
     "moe_ffn_workspace_layout", "moe_expert_ffn_forward",
     "moe_expert_ffn_forward_timed", "moe_expert_ffn_forward_presorted", "moe_router_topk",
     "moe_status_string", "moe_expert_ffn_forward_noalloc", "moe_block_norm",
-    "moe_router_forward", "moe_layer_workspace_bytes", "moe_layer_forward",
+    "moe_router_forward", "moe_layer_workspace_bytes", "moe_layer_forward", "moe_grouped_matmul",
+    "moe_grouped_dw_workspace_bytes", "moe_grouped_matmul_dw", "moe_mx_quantize", "moe_mx_dequantize",
 )
 MOE_ERR_SCRATCH = -7
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -106,6 +110,15 @@ def lib():
         L.moe_layer_forward.argtypes = [ctypes.POINTER(MoeProblem), ctypes.POINTER(MoeLayerDesc), P,
                                         ctypes.POINTER(MoeNorm), P, sz, P]
         L.moe_layer_forward.restype = i32
+        L.moe_grouped_matmul.argtypes = [ctypes.POINTER(MoeGrouped), P]
+        L.moe_grouped_matmul.restype = i32
+        L.moe_grouped_dw_workspace_bytes.argtypes = [ctypes.POINTER(MoeGroupedGrad)]
+        L.moe_grouped_dw_workspace_bytes.restype = sz
+        L.moe_grouped_matmul_dw.argtypes = [ctypes.POINTER(MoeGroupedGrad), P, sz, P]
+        L.moe_grouped_matmul_dw.restype = i32
+        for f in (L.moe_mx_quantize, L.moe_mx_dequantize):
+            f.argtypes = [ctypes.POINTER(MoeMx), P]
+            f.restype = i32
         _lib = L
     return _lib
 

@@ -1,0 +1,157 @@
+// C ABI of the products grouped by expert and of the microscaled values: argument checks,
+// then the launches.
+#include <limits.h>
+
+#include "moe_internal.h"
+
+namespace {
+
+bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool plain_type(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP32; }
+// A row stride of an input: 16-byte steps, 32-bit offsets inside a tile.
+bool input_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s <= MOE_GROUPED_MAX_STRIDE; }
+
+moe_status check_sizes(int32_t A, int32_t E, int32_t N, int32_t K, int32_t step) {
+    if (A < 0 || A >= 1 << 30 || E < 1 || N < 1 || K < 1 || N % 8 || K % step) return MOE_ERR_SHAPE;
+    if (E > MOE_MAX_EXPERTS || N > MOE_GROUPED_MAX_DIM || K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status check(const moe_grouped* g) {
+    if (!g) return MOE_ERR_NULL;
+    const bool xm = g->x_type == MOE_T_MXFP4, wm = g->w_type == MOE_T_MXFP4, kn = g->flags & MOE_G_W_KN;
+    if ((!xm && g->x_type != MOE_T_BF16) || (!wm && g->w_type != MOE_T_BF16) || (xm && !wm) || !plain_type(g->out_type) ||
+        (g->flags & ~MOE_G_W_KN) || (kn && wm))
+        return MOE_ERR_UNSUPPORTED;
+    const moe_status st = check_sizes(g->A, g->E, g->N, g->K, wm ? 32 : 8);
+    if (st != MOE_OK) return st;
+    // workgroups of the smallest tile any form takes
+    if ((static_cast<int64_t>(g->A) / 16 + g->E) * ((g->N + 31) / 32) >= INT32_MAX) return MOE_ERR_SHAPE;
+    if (!xm && !input_stride(g->x_stride)) return MOE_ERR_SHAPE;
+    if (!wm && (!input_stride(g->w_stride) || g->w_expert_stride < 0 || g->w_expert_stride % 8)) return MOE_ERR_SHAPE;
+    if (g->out_stride < g->N || g->out_stride > MOE_GROUPED_MAX_STRIDE || g->out_stride % (g->out_type == MOE_T_FP32 ? 4 : 8))
+        return MOE_ERR_SHAPE;
+    if (g->A == 0) return MOE_OK;
+    if (!g->x || !g->w || !g->out || (!g->offsets && g->E > 1) || (xm && !g->x_scales) || (wm && !g->w_scales))
+        return MOE_ERR_NULL;
+    if (!on(g->x, 16) || !on(g->w, 16) || !on(g->out, 16) || !on(g->offsets, 4)) return MOE_ERR_ALIGN;
+    return g->out == g->x || g->out == g->w ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// Sizes of a gradient of the weights: what the workspace depends on.
+moe_status check_grad_sizes(const moe_grouped_grad* g) {
+    const moe_status st = check_sizes(g->A, g->E, g->N, g->K, 8);
+    if (st != MOE_OK) return st;
+    return static_cast<int64_t>(g->E) * ((g->N + 63) / 64) * ((g->K + 63) / 64) >= INT32_MAX ? MOE_ERR_SHAPE : MOE_OK;
+}
+
+moe_status check(const moe_grouped_grad* g) {
+    if (!g) return MOE_ERR_NULL;
+    if (!plain_type(g->out_type)) return MOE_ERR_UNSUPPORTED;
+    const moe_status st = check_grad_sizes(g);
+    if (st != MOE_OK) return st;
+    if (!input_stride(g->dy_stride) || !input_stride(g->x_stride)) return MOE_ERR_SHAPE;
+    // without rows dw is zeros all the same
+    if (!g->dw || (!g->offsets && g->E > 1) || (g->A > 0 && (!g->dy || !g->x))) return MOE_ERR_NULL;
+    if (!on(g->dy, 16) || !on(g->x, 16) || !on(g->dw, 16) || !on(g->offsets, 4)) return MOE_ERR_ALIGN;
+    return g->dw == g->dy || g->dw == g->x ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status check(const moe_mx* q, bool quantize) {
+    if (!q) return MOE_ERR_NULL;
+    if (!plain_type(q->type) || (q->flags & ~(MOE_Q_GELU | MOE_Q_SILU)) || q->flags == (MOE_Q_GELU | MOE_Q_SILU) ||
+        (!quantize && q->flags))
+        return MOE_ERR_UNSUPPORTED;
+    if (q->R < 0 || q->K < 1 || q->K % 32) return MOE_ERR_SHAPE;
+    if (q->K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+    if (q->R >= (int64_t{1} << 34) / q->K) return MOE_ERR_SHAPE;
+    const int64_t row = q->flags ? 2 * static_cast<int64_t>(q->K) : q->K;
+    if (q->stride < row || q->stride % (q->type == MOE_T_FP32 ? 4 : 8) || q->stride > int64_t{1} << 30) return MOE_ERR_SHAPE;
+    if (q->R == 0) return MOE_OK;
+    if (!q->values || !q->codes || !q->scales) return MOE_ERR_NULL;
+    return on(q->values, 16) && on(q->codes, 16) ? MOE_OK : MOE_ERR_ALIGN;
+}
+
+moe::MxArgs mx_args(const moe_mx* q) {
+    moe::MxArgs a = {};
+    a.R = q->R;
+    a.K = q->K;
+    a.f32 = q->type == MOE_T_FP32;
+    a.glu = q->flags & MOE_Q_GELU ? 1 : q->flags & MOE_Q_SILU ? 2 : 0;
+    a.values = q->values;
+    a.codes = q->codes;
+    a.scales = q->scales;
+    a.stride = q->stride * (a.f32 ? 4 : 2);
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_matmul(const moe_grouped* g, void* stream) {
+    const moe_status st = check(g);
+    if (st != MOE_OK || g->A == 0) return st;
+    moe::GroupedArgs a = {};
+    a.A = g->A;
+    a.E = g->E;
+    a.N = g->N;
+    a.K = g->K;
+    a.w_kn = g->flags & MOE_G_W_KN;
+    a.out_f32 = g->out_type == MOE_T_FP32;
+    a.offsets = g->offsets;
+    a.x = g->x;
+    a.w = g->w;
+    a.xs = g->x_scales;
+    a.ws = g->w_scales;
+    a.out = g->out;
+    a.x_stride = 2 * g->x_stride;
+    a.w_stride = 2 * g->w_stride;
+    a.w_expert = 2 * g->w_expert_stride;
+    a.out_stride = g->out_stride * (a.out_f32 ? 4 : 2);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const hipError_t e = g->w_type == MOE_T_BF16   ? moe::launch_grouped_bf16(a, s)
+                         : g->x_type == MOE_T_BF16 ? moe::launch_grouped_bf16_mx(a, s)
+                                                   : moe::launch_grouped_mx(a, s);
+    return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+size_t moe_grouped_dw_workspace_bytes(const moe_grouped_grad* g) {
+    return g && check_grad_sizes(g) == MOE_OK ? moe::grouped_dw_workspace(g->A, g->E, g->N, g->K) : 0;
+}
+
+moe_status moe_grouped_matmul_dw(const moe_grouped_grad* g, void* ws, size_t ws_bytes, void* stream) {
+    const moe_status st = check(g);
+    if (st != MOE_OK) return st;
+    const size_t need = moe::grouped_dw_workspace(g->A, g->E, g->N, g->K);
+    if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (need > 0 && !on(ws, 256)) return MOE_ERR_ALIGN;
+    moe::GroupedGradArgs a = {};
+    a.A = g->A;
+    a.E = g->E;
+    a.N = g->N;
+    a.K = g->K;
+    a.out_f32 = g->out_type == MOE_T_FP32;
+    a.offsets = g->offsets;
+    a.dy = g->dy;
+    a.x = g->x;
+    a.dw = g->dw;
+    a.dy_stride = 2 * g->dy_stride;
+    a.x_stride = 2 * g->x_stride;
+    a.ws = static_cast<float*>(ws);
+    return moe::launch_grouped_dw(a, static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_mx_quantize(const moe_mx* q, void* stream) {
+    const moe_status st = check(q, true);
+    if (st != MOE_OK || q->R == 0) return st;
+    return moe::launch_mx_quantize(mx_args(q), static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_mx_dequantize(const moe_mx* q, void* stream) {
+    const moe_status st = check(q, false);
+    if (st != MOE_OK || q->R == 0) return st;
+    return moe::launch_mx_dequantize(mx_args(q), static_cast<hipStream_t>(stream)) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"

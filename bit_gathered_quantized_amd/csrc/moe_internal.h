@@ -359,4 +359,44 @@ struct LayerArgs {
 };
 hipError_t launch_layer_few(const LayerArgs& a, hipStream_t stream);
 
+// Products grouped by expert (grouped_*.hip); sizes and pointers as in moe_grouped.
+struct GroupedArgs {
+    int32_t A, E, N, K;
+    bool w_kn, out_f32;
+    const int32_t* offsets;  // nullptr: one expert with all rows
+    const void *x, *w;
+    const uint8_t *xs, *ws;
+    void* out;
+    int64_t x_stride, w_stride, w_expert, out_stride;  // bytes
+};
+hipError_t launch_grouped_bf16(const GroupedArgs& a, hipStream_t stream);
+hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
+hipError_t launch_grouped_bf16_mx(const GroupedArgs& a, hipStream_t stream);
+
+// The gradient of the experts' weights (grouped_dw.hip).
+struct GroupedGradArgs {
+    int32_t A, E, N, K;
+    bool out_f32;
+    const int32_t* offsets;
+    const void *dy, *x;
+    void* dw;
+    int64_t dy_stride, x_stride;  // bytes
+    float* ws;
+};
+size_t grouped_dw_workspace(int32_t A, int32_t E, int32_t N, int32_t K);
+hipError_t launch_grouped_dw(const GroupedGradArgs& a, hipStream_t stream);
+
+// Microscaled values (mx.hip).
+struct MxArgs {
+    int64_t R;
+    int32_t K;
+    bool f32;
+    int glu;  // 0 none, 1 GELU, 2 SiLU
+    void* values;
+    uint8_t *codes, *scales;
+    int64_t stride;  // bytes
+};
+hipError_t launch_mx_quantize(const MxArgs& a, hipStream_t stream);
+hipError_t launch_mx_dequantize(const MxArgs& a, hipStream_t stream);
+
 }  // namespace moe

@@ -337,7 +337,8 @@ moe_status moe_expert_ffn_forward_timed(const moe_problem* p, const void* x,
 /* Element types of the tensors below. */
 enum {
     MOE_T_BF16 = 0,
-    MOE_T_FP32 = 1
+    MOE_T_FP32 = 1,
+    MOE_T_MXFP4 = 2 /* microscaled 4-bit values (moe_mx_quantize); operands of moe_grouped_matmul only */
 };
 
 /*
@@ -475,6 +476,119 @@ size_t moe_layer_workspace_bytes(const moe_problem* p);
  * the outputs of both are undefined). */
 moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const void* x, const moe_norm* tail,
                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Products grouped by expert.  The rows of x are sorted by expert, as perm of
+ * moe_sort_build_tiles puts them; expert e has the rows [offsets[e], offsets[e + 1]).
+ *
+ *   out[r, n] = sum_k x[r, k] w[e, n, k]     w [E, N, K]
+ *             = sum_k x[r, k] w[e, k, n]     w [E, K, N], with MOE_G_W_KN
+ *
+ * The second form is the gradient of the rows: with dy [A, N] and the forward's w
+ * [E, N, K] it gives dx [A, K].  Products are exact, sums fp32, out is rounded once.
+ * A row's result depends on that row and its expert alone.  Rows outside
+ * [offsets[0], offsets[E]) are not written.
+ *
+ * x and w are bf16, or microscaled 4-bit values: both, or w alone.  Microscaled rows
+ * are the codes [.., K / 2] and scales [.., K / 32] of moe_mx_quantize, contiguous; they
+ * do not go with MOE_G_W_KN (the scales lie along K).
+ */
+#define MOE_G_W_KN 1u
+#define MOE_GROUPED_MAX_STRIDE (1 << 22)
+#define MOE_GROUPED_MAX_DIM (1 << 20)
+typedef struct {
+    int32_t A;                 /* rows, 0 <= A < 2^30                                  */
+    int32_t E;                 /* experts, 1 <= E <= MOE_MAX_EXPERTS                   */
+    int32_t N;                 /* columns of out: a multiple of 8, <= MOE_GROUPED_MAX_DIM */
+    int32_t K;                 /* length of a sum: a multiple of 8 (microscaled w: of
+                                  32), <= MOE_GROUPED_MAX_DIM                          */
+    int32_t x_type;            /* MOE_T_BF16 or MOE_T_MXFP4                            */
+    int32_t w_type;            /* MOE_T_BF16 or MOE_T_MXFP4                            */
+    int32_t out_type;          /* MOE_T_BF16 or MOE_T_FP32                             */
+    uint32_t flags;            /* MOE_G_*                                              */
+    const int32_t* offsets;    /* [E + 1], non-decreasing, within [0, A]; others give
+                                  wrong or missing rows, but nothing outside of x, w
+                                  and out is touched.  NULL with E = 1: all rows       */
+    const void* x;             /* bf16 [A, K] or codes [A, K / 2]                      */
+    const void* w;             /* bf16 [E, N, K] ([E, K, N]) or codes [E, N, K / 2]    */
+    const uint8_t* x_scales;   /* [A, K / 32] of microscaled x, else NULL              */
+    const uint8_t* w_scales;   /* [E, N, K / 32] of microscaled w, else NULL           */
+    void* out;                 /* [A, N]                                               */
+    int64_t x_stride;          /* elements from one row of bf16 x to the next, a multiple
+                                  of 8 in [0, MOE_GROUPED_MAX_STRIDE] (microscaled x:
+                                  not used)                                            */
+    int64_t w_stride;          /* the same for the rows of w                           */
+    int64_t w_expert_stride;   /* elements from one expert of bf16 w to the next, a
+                                  multiple of 8, >= 0                                  */
+    int64_t out_stride;        /* a multiple of 8 (fp32: of 4), >= N, <= MOE_GROUPED_MAX_STRIDE */
+} moe_grouped;
+
+/* x, w and out start on 16 bytes and out lies on none of the inputs.  Deterministic;
+ * needs no workspace. */
+moe_status moe_grouped_matmul(const moe_grouped* g, void* stream);
+
+/*
+ * The gradient of the experts' weights:  dw[e, n, k] = sum over the rows r of e of
+ * dy[r, n] x[r, k], zeros for an expert without rows.  Products exact, sums fp32,
+ * rounded once.
+ */
+typedef struct {
+    int32_t A;                 /* as in moe_grouped                                    */
+    int32_t E;
+    int32_t N;                 /* columns of dy and K of x: multiples of 8,            */
+    int32_t K;                 /* <= MOE_GROUPED_MAX_DIM                               */
+    int32_t out_type;          /* MOE_T_BF16 or MOE_T_FP32                             */
+    const int32_t* offsets;    /* as in moe_grouped                                    */
+    const void* dy;            /* bf16 [A, N]                                          */
+    const void* x;             /* bf16 [A, K]                                          */
+    void* dw;                  /* [E, N, K], contiguous                                */
+    int64_t dy_stride;         /* elements from one row to the next, a multiple of 8,  */
+    int64_t x_stride;          /* in [0, MOE_GROUPED_MAX_STRIDE]                       */
+} moe_grouped_grad;
+
+/* Device workspace of moe_grouped_matmul_dw: 0 where it needs none, or on invalid
+ * sizes.  A function of A, E, N and K alone. */
+size_t moe_grouped_dw_workspace_bytes(const moe_grouped_grad* g);
+
+/* dy, x and dw start on 16 bytes; ws: moe_grouped_dw_workspace_bytes(g) bytes, 256-byte
+ * aligned, with any contents (NULL where that is 0); one call at a time may use it.
+ * Deterministic. */
+moe_status moe_grouped_matmul_dw(const moe_grouped_grad* g, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit values.  Blocks of 32 values along a row share a scale 2^s, held
+ * as the byte s + 127; a value is a code of 1 sign bit, 2 exponent bits and 1 mantissa
+ * bit (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte, the first in the
+ * low four bits.
+ *
+ *   s    = floor(log2(max |v|)) - 2, at least -127   (a block of zeros: -127)
+ *   code = v / 2^s, to nearest, ties to the even code, |v| / 2^s over 6 as 6
+ *
+ * A block that holds a NaN or an infinity gets the byte 255, and all of it stands for
+ * NaN.  With MOE_Q_GELU or MOE_Q_SILU a row of x holds 2 K values [g | u] and
+ * v = act(g) u (fp32; the tanh GELU and SiLU of the expert FFN), else v = x.
+ */
+#define MOE_Q_GELU 1u
+#define MOE_Q_SILU 2u
+typedef struct {
+    int64_t R;                 /* rows, >= 0, R K < 2^34                               */
+    int32_t K;                 /* values of a row: a multiple of 32, <= MOE_GROUPED_MAX_DIM */
+    int32_t type;              /* MOE_T_* of the values: BF16 or FP32                  */
+    uint32_t flags;            /* MOE_Q_* (quantising)                                 */
+    void* values;              /* [R, K]; quantising with MOE_Q_GELU or MOE_Q_SILU [R, 2 K] */
+    uint8_t* codes;            /* [R, K / 2], contiguous                               */
+    uint8_t* scales;           /* [R, K / 32], contiguous                              */
+    int64_t stride;            /* elements from one row of values to the next, a multiple
+                                  of 8 (fp32: of 4), at least a row                    */
+} moe_mx;
+
+/* values -> codes and scales.  values and codes start on 16 bytes.  The values are not
+ * written. */
+moe_status moe_mx_quantize(const moe_mx* q, void* stream);
+
+/* codes and scales -> values, exact in both types (past their range infinity; the byte 255
+ * gives NaN). */
+moe_status moe_mx_dequantize(const moe_mx* q, void* stream);
 
 /* Static description of a status code. */
 const char* moe_status_string(moe_status s);
