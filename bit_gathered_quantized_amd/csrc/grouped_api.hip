@@ -25,8 +25,8 @@ moe_status check(const moe_grouped* g) {
         return MOE_ERR_UNSUPPORTED;
     const moe_status st = check_sizes(g->A, g->E, g->N, g->K, wm ? 32 : 8);
     if (st != MOE_OK) return st;
-    // workgroups of the smallest tile any form takes
-    if ((static_cast<int64_t>(g->A) / 16 + g->E) * ((g->N + 31) / 32) >= INT32_MAX) return MOE_ERR_SHAPE;
+    // tiles of 64 rows by 64 columns: the kernels' sums over them stay within 32 bits
+    if ((static_cast<int64_t>(g->A) / 64 + g->E) * ((g->N + 63) / 64) >= 1 << 24) return MOE_ERR_SHAPE;
     if (!xm && !input_stride(g->x_stride)) return MOE_ERR_SHAPE;
     if (!wm && (!input_stride(g->w_stride) || g->w_expert_stride < 0 || g->w_expert_stride % 8)) return MOE_ERR_SHAPE;
     if (g->out_stride < g->N || g->out_stride > MOE_GROUPED_MAX_STRIDE || g->out_stride % (g->out_type == MOE_T_FP32 ? 4 : 8))
@@ -102,15 +102,16 @@ moe_status moe_grouped_matmul(const moe_grouped* g, void* stream) {
     a.offsets = g->offsets;
     a.x = g->x;
     a.w = g->w;
-    a.xs = g->x_scales;
-    a.ws = g->w_scales;
+    a.xs = g->x_type == MOE_T_MXFP4 ? g->x_scales : nullptr;
+    a.ws = g->w_type == MOE_T_MXFP4 ? g->w_scales : nullptr;
     a.out = g->out;
     a.x_stride = 2 * g->x_stride;
     a.w_stride = 2 * g->w_stride;
     a.w_expert = 2 * g->w_expert_stride;
     a.out_stride = g->out_stride * (a.out_f32 ? 4 : 2);
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const hipError_t e = g->w_type == MOE_T_BF16   ? moe::launch_grouped_bf16(a, s)
+    const hipError_t e = moe::grouped_few_rows(a)    ? moe::launch_grouped_few(a, s)
+                         : g->w_type == MOE_T_BF16 ? moe::launch_grouped_bf16(a, s)
                          : g->x_type == MOE_T_BF16 ? moe::launch_grouped_bf16_mx(a, s)
                                                    : moe::launch_grouped_mx(a, s);
     return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -1,8 +1,11 @@
 // The gradient of the experts' weights:  dw[e, n, k] = sum over the rows r of expert e of
 // dy[r, n] x[r, k].
 //
-// The sum runs along the rows, across both operands' memory: tiles of 64 rows come to LDS
-// as they lie and the reads turn them.
+// The sum runs along the rows, across both operands' memory: stages of 64 rows come to LDS
+// as they lie and the reads turn them.  One workgroup a CU takes its tiles in turn; four of
+// its waves only copy, D - 1 stages ahead, and eight multiply and store.  So nothing waits
+// at a tile's end: a wave's memory operations end in order, and with copies and stores in one
+// wave the next stage would wait for the last tile's stores.
 #include "grouped.h"
 
 namespace moe {
@@ -10,124 +13,200 @@ namespace {
 
 using namespace grouped;
 
-// Pieces of 32 bytes of row r (mod 64) are XORed with r, for the turning reads: four rows
-// at a time.
-template <int BN, int BK, int WN, int WK, bool kF32>
-__global__ __launch_bounds__(64 * WN * WK) void moe_grouped_dw_tile(GroupedGradArgs a, uint32_t tiles_n, uint32_t tiles_k,
-                                                                   uint32_t splits) {
-    constexpr int kWaves = WN * WK, FN = BN / WN / 16, FK = BK / WK / 16;
-    constexpr int kYJobs = BN / 8 / kWaves, kXJobs = BK / 8 / kWaves;
-    static_assert(kYJobs * 8 * kWaves == BN && kXJobs * 8 * kWaves == BK, "tile");
-    __shared__ __align__(16) unsigned char y0[BN * 128], y1[BN * 128], x0[BK * 128], x1[BK * 128];
-    const uint32_t index = grid_index();
-    // a run of neighbouring tiles for each XCD: those of an expert read the same rows
-    const uint32_t tiles = tiles_n * tiles_k * a.E * splits, share = (tiles + 7) / 8;
-    const uint32_t number = (index & 7) * share + (index >> 3);
-    if ((index >> 3) >= share || number >= tiles) return;
-    const uint32_t of_expert = tiles_n * tiles_k, whole = number / splits, split = number - whole * splits;
-    const int expert = whole / of_expert;
-    const uint32_t rest = whole - expert * of_expert;
-    const int k0 = (rest / tiles_n) * BK, n0 = (rest % tiles_n) * BN;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int lr = lane & 15, q = lane >> 4, wk = wave / WN, wn = wave % WN;
-    int begin = 0, end = a.A;
-    if (a.offsets) expert_rows(a.offsets, expert, a.E, a.A, begin, end);
-    const int stages_all = (end - begin + 63) / 64;
-    const int s0 = static_cast<int>(static_cast<int64_t>(stages_all) * split / splits);
-    const int s1 = static_cast<int>(static_cast<int64_t>(stages_all) * (split + 1) / splits);
-    const int ycols = min(BN, a.N - n0), xcols = min(BK, a.K - k0);
+struct DwTiles {
+    uint32_t n, k, splits, count;  // blocks of columns of dy and of x, runs of an expert's rows, all tiles
+};
 
-    uint32_t yat[kYJobs], xat[kXJobs];
-    int yrow[kYJobs], xrow[kXJobs];
-#pragma unroll
-    for (int j = 0; j < kYJobs; ++j) {
-        constexpr int kPieces = BN / 8;
-        yrow[j] = 64 / kPieces * (j * kWaves + wave) + lane / kPieces;
-        const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (yrow[j] & 7)) + 16 * (p & 1);
-        yat[j] = col < 2 * ycols ? static_cast<uint32_t>(yrow[j]) * static_cast<uint32_t>(a.dy_stride) + col : kOutside;
-    }
-#pragma unroll
-    for (int j = 0; j < kXJobs; ++j) {
-        constexpr int kPieces = BK / 8;
-        xrow[j] = 64 / kPieces * (j * kWaves + wave) + lane / kPieces;
-        const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (xrow[j] & 7)) + 16 * (p & 1);
-        xat[j] = col < 2 * xcols ? static_cast<uint32_t>(xrow[j]) * static_cast<uint32_t>(a.x_stride) + col : kOutside;
-    }
-    auto issue = [&](unsigned char* ys, unsigned char* xs, int s) {
-        const int first = begin + 64 * s, rows = min(64, end - first);
-        const Rsrc ry = make_rsrc(static_cast<const unsigned char*>(a.dy) + first * a.dy_stride + 2 * static_cast<int64_t>(n0),
-                                  static_cast<uint32_t>((rows - 1) * a.dy_stride) + 2 * ycols);
-        const Rsrc rx = make_rsrc(static_cast<const unsigned char*>(a.x) + first * a.x_stride + 2 * static_cast<int64_t>(k0),
-                                  static_cast<uint32_t>((rows - 1) * a.x_stride) + 2 * xcols);
-        // rows past the expert's last read zeros
-#pragma unroll
-        for (int j = 0; j < kYJobs; ++j) copy16(ry, ys + 1024 * (j * kWaves + wave), yrow[j] < rows ? yat[j] : kOutside, 0);
-#pragma unroll
-        for (int j = 0; j < kXJobs; ++j) copy16(rx, xs + 1024 * (j * kWaves + wave), xrow[j] < rows ? xat[j] : kOutside, 0);
+// Pieces of 32 bytes of row r of a stage are XORed with r, for the turning reads: four rows
+// at a time.
+template <int BN, int BK, int WN, int WK, int D, bool kF32>
+__global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(GroupedGradArgs a, DwTiles tiles) {
+    constexpr int kWaves = WN * WK, kLoaders = 4, FN = BN / WN / 16, FK = BK / WK / 16, kStage = 64;
+    constexpr int kYJobs = BN / 8 / kLoaders, kXJobs = BK / 8 / kLoaders, kJobs = kYJobs + kXJobs;
+    static_assert(kYJobs * 8 * kLoaders == BN && kXJobs * 8 * kLoaders == BK && FK % 2 == 0, "tile");
+    __shared__ __align__(16) unsigned char ybuf[D][BN * 128], xbuf[D][BK * 128];
+    __shared__ __align__(16) unsigned char turn[kWaves][16 * 128];  // results on their way out
+    // Tiles are dealt out within each XCD's run of neighbours (workgroups go to the XCDs in
+    // turn): those at work at a time read the same rows.
+    const uint32_t share = (tiles.count + 7) / 8, first = (blockIdx.x & 7) * share + (blockIdx.x >> 3);
+    const uint32_t end = min((blockIdx.x & 7) * share + share, tiles.count), step_by = gridDim.x >> 3;
+    if (first >= end) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    struct Tile {
+        int expert, split, n0, k0, row, rows;  // rows [row, row + rows) of dy and x
+        int stages;
     };
+    auto find = [&](uint32_t number) {
+        const uint32_t whole = number / tiles.splits, of_expert = tiles.n * tiles.k;
+        Tile t;
+        t.split = __builtin_amdgcn_readfirstlane(static_cast<int>(number - whole * tiles.splits));
+        t.expert = __builtin_amdgcn_readfirstlane(static_cast<int>(whole / of_expert));
+        const uint32_t rest = whole - t.expert * of_expert, kb = rest / tiles.n;
+        t.k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(kb * BK));
+        t.n0 = __builtin_amdgcn_readfirstlane(static_cast<int>((rest - kb * tiles.n) * BN));
+        int lo = 0, hi = a.A;
+        if (a.offsets) {  // through the scalar cache: a vector load would wait for the copies before it
+            const auto* const o = (const __attribute__((address_space(4))) int32_t*)a.offsets;
+            lo = min(max(o[t.expert], 0), a.A);
+            hi = min(max(o[t.expert + 1], lo), a.A);
+        }
+        if (tiles.splits > 1) {  // whole stages
+            const int64_t all = (hi - lo + kStage - 1) / kStage;
+            const int from = lo + kStage * static_cast<int>(all * t.split / static_cast<int>(tiles.splits));
+            hi = min(hi, lo + kStage * static_cast<int>(all * (t.split + 1) / static_cast<int>(tiles.splits)));
+            lo = min(from, hi);
+        }
+        t.row = __builtin_amdgcn_readfirstlane(lo);
+        t.rows = __builtin_amdgcn_readfirstlane(hi - lo);
+        t.stages = max((t.rows + kStage - 1) / kStage, 1);  // without rows one of zeros
+        return t;
+    };
+
+    // A stage is a step: the copiers wait for its copies, then all waves meet, then the
+    // copiers start the stage D - 1 steps ahead, in the buffer of the last step.
+    if (wave >= kWaves) {
+        const int w = wave - kWaves;
+        uint32_t ahead = first, steps = 0;  // steps: those whose copies are under way
+        Tile t = find(ahead);
+        int stage = 0, buffer = 0;
+        uint32_t yat[kYJobs], xat[kXJobs];
+        int yrow[kYJobs], xrow[kXJobs];
+        auto aim = [&] {
+            const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
+#pragma unroll
+            for (int j = 0; j < kYJobs; ++j) {
+                constexpr int kPieces = BN / 8;
+                yrow[j] = 64 / kPieces * (j * kLoaders + w) + lane / kPieces;
+                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (yrow[j] & 7)) + 16 * (p & 1);
+                yat[j] = col < 2 * ycols ? static_cast<uint32_t>(yrow[j]) * static_cast<uint32_t>(a.dy_stride) + col : kOutside;
+            }
+#pragma unroll
+            for (int j = 0; j < kXJobs; ++j) {
+                constexpr int kPieces = BK / 8;
+                xrow[j] = 64 / kPieces * (j * kLoaders + w) + lane / kPieces;
+                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (xrow[j] & 7)) + 16 * (p & 1);
+                xat[j] = col < 2 * xcols ? static_cast<uint32_t>(xrow[j]) * static_cast<uint32_t>(a.x_stride) + col : kOutside;
+            }
+        };
+        auto issue = [&] {
+            // rows past the expert's last read zeros
+            const int from = t.row + kStage * stage, rows = min(kStage, t.rows - kStage * stage);
+            const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
+            const Rsrc ry = make_rsrc(static_cast<const unsigned char*>(a.dy) + from * a.dy_stride + 2 * static_cast<int64_t>(t.n0),
+                                      static_cast<uint32_t>(max(rows - 1, 0) * a.dy_stride) + 2 * ycols);
+            const Rsrc rx = make_rsrc(static_cast<const unsigned char*>(a.x) + from * a.x_stride + 2 * static_cast<int64_t>(t.k0),
+                                      static_cast<uint32_t>(max(rows - 1, 0) * a.x_stride) + 2 * xcols);
+#pragma unroll
+            for (int j = 0; j < kYJobs; ++j)
+                copy16(ry, ybuf[buffer] + 1024 * (j * kLoaders + w), yrow[j] < rows ? yat[j] : kOutside, 0);
+#pragma unroll
+            for (int j = 0; j < kXJobs; ++j)
+                copy16(rx, xbuf[buffer] + 1024 * (j * kLoaders + w), xrow[j] < rows ? xat[j] : kOutside, 0);
+            buffer = buffer + 1 == D ? 0 : buffer + 1;
+            ++steps;
+            if (++stage == t.stages) {
+                stage = 0;
+                ahead += step_by;
+                if (ahead < end) {
+                    t = find(ahead);
+                    aim();
+                }
+            }
+        };
+        aim();
+        for (int i = 0; i < D - 1 && ahead < end; ++i) issue();
+        for (uint32_t at = 0; at < steps; ++at) {
+            if (ahead < end)
+                wait_copies<(D - 2) * kJobs>();
+            else
+                wait_copies<0>();
+            step_barrier();
+            if (ahead < end) issue();
+        }
+        return;
+    }
+
+    const int lr = lane & 15, q = lane >> 4, wk = wave / WN, wn = wave % WN;
     f32x4 acc[FN][FK];
-#pragma unroll
-    for (int n = 0; n < FN; ++n)
-#pragma unroll
-        for (int k = 0; k < FK; ++k) acc[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int r = 8 * q + (lr >> 2);
     int yturn[FN], xturn[FK];
 #pragma unroll
     for (int n = 0; n < FN; ++n) yturn[n] = r * 2 * BN + 32 * ((wn * FN + n) ^ (r & 7)) + 8 * (lr & 3);
 #pragma unroll
     for (int k = 0; k < FK; ++k) xturn[k] = r * 2 * BK + 32 * ((wk * FK + k) ^ (r & 7)) + 8 * (lr & 3);
-    auto compute = [&](const unsigned char* ys, const unsigned char* xs) {
+    int buffer = 0;
+    for (uint32_t here = first; here < end; here += step_by) {
+        const Tile t = find(here);
+        const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
+        // whether this wave's part of the tile holds anything
+        const bool active = 16 * wn * FN < ycols && 16 * wk * FK < xcols;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            u32x4 yf[FN], xf[FK];
-            // rows + 4: the XOR turns over bit 2, as that of the piece's number with 4 does
+        for (int n = 0; n < FN; ++n)
 #pragma unroll
-            for (int n = 0; n < FN; ++n) {
-                const u32x2 lo = read_turned(ys, yturn[n] + 64 * s * BN), hi = read_turned(ys, (yturn[n] ^ 128) + 64 * s * BN + 8 * BN);
-                yf[n] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+            for (int k = 0; k < FK; ++k) acc[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int stage = 0; stage < t.stages; ++stage) {
+            step_barrier();
+            const unsigned char *const ys = ybuf[buffer], *const xs = xbuf[buffer];
+            buffer = buffer + 1 == D ? 0 : buffer + 1;
+            if (!active) continue;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                u32x4 yf[FN], xf[FK];
+                // rows + 4: the XOR turns over bit 2, as that of the piece's number with 4 does
+#pragma unroll
+                for (int n = 0; n < FN; ++n) {
+                    const u32x2 lo = read_turned(ys, yturn[n] + 64 * s * BN), hi = read_turned(ys, (yturn[n] ^ 128) + 64 * s * BN + 8 * BN);
+                    yf[n] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                }
+#pragma unroll
+                for (int k = 0; k < FK; ++k) {
+                    const u32x2 lo = read_turned(xs, xturn[k] + 64 * s * BK), hi = read_turned(xs, (xturn[k] ^ 128) + 64 * s * BK + 8 * BK);
+                    xf[k] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                }
+#pragma unroll
+                for (int n = 0; n < FN; ++n)
+#pragma unroll
+                    for (int k = 0; k < FK; ++k) acc[n][k] = mfma_bf16(xf[k], yf[n], acc[n][k]);
             }
+        }
+        // A product's lanes hold 16 rows of n; memory wants rows of 128 bytes.  So 16 rows of
+        // 128 bytes at a time go through LDS, pieces of 16 bytes XORed with the row (a wave's
+        // own: no barrier).  Storing the products as they lie, 64 bytes of 16 rows an
+        // instruction, measured 380 | 343 us at 16384 rows of 128 experts by 1408 x 2816.
+        constexpr int kOut = kF32 ? 4 : 2, kBlock = 128 / (16 * kOut);  // products in 128 bytes
+        unsigned char* const out = static_cast<unsigned char*>(a.dw) +
+                                   kOut * (((static_cast<int64_t>(t.split) * a.E + t.expert) * a.N + t.n0) * a.K + t.k0);
+        const uint32_t pitch = static_cast<uint32_t>(kOut * a.K);
+        const Rsrc ro = make_rsrc(out, (ycols - 1) * pitch + kOut * xcols);
+        unsigned char* const mine = turn[wave];
 #pragma unroll
-            for (int k = 0; k < FK; ++k) {
-                const u32x2 lo = read_turned(xs, xturn[k] + 64 * s * BK), hi = read_turned(xs, (xturn[k] ^ 128) + 64 * s * BK + 8 * BK);
-                xf[k] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        for (int n = 0; n < FN; ++n) {
+#pragma unroll
+            for (int k = 0; k < FK; k += kBlock) {
+#pragma unroll
+                for (int i = 0; i < kBlock; i += kF32 ? 1 : 2) {
+                    u32x4 v;
+                    int piece;
+                    if constexpr (kF32) {
+                        v = __builtin_bit_cast(u32x4, acc[n][k + i]);
+                        piece = 4 * i + q;
+                    } else {
+                        v = eight_bf16(acc[n][k + i], acc[n][k + i + 1]);
+                        piece = 2 * (i + (q & 1)) + (q >> 1);
+                    }
+                    *reinterpret_cast<u32x4*>(mine + 128 * lr + 16 * (piece ^ (lr & 7))) = v;
+                }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int r = 8 * half + (lane >> 3), p = lane & 7;
+                    const u32x4 v = read16(mine, 128 * r + 16 * (p ^ (r & 7)));
+                    const int row = 16 * (wn * FN + n) + r, col = 16 * (wk * FK + k) + p * (16 / kOut);
+                    store16(ro, v, row < ycols && col < xcols ? static_cast<uint32_t>(row) * pitch + kOut * col : kOutside);
+                }
+                __builtin_amdgcn_wave_barrier();
             }
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int k = 0; k < FK; ++k) acc[n][k] = mfma_bf16(xf[k], yf[n], acc[n][k]);
-        }
-    };
-    if (s0 < s1) {
-        issue(y0, x0, s0);
-        copies_done<0>();
-        for (int s = s0; s < s1; s += 2) {
-            if (s + 1 < s1) issue(y1, x1, s + 1);
-            compute(y0, x0);
-            copies_done<0>();
-            if (s + 1 >= s1) break;
-            if (s + 2 < s1) issue(y0, x0, s + 2);
-            compute(y1, x1);
-            copies_done<0>();
-        }
-    }
-    // lane (lr, q) of a product holds columns 4 q .. 4 q + 3 of k and row lr of n
-    constexpr int kOut = kF32 ? 4 : 2;
-    unsigned char* const out = static_cast<unsigned char*>(a.dw) +
-                               kOut * (((static_cast<int64_t>(split) * a.E + expert) * a.N + n0) * a.K + k0);
-#pragma unroll
-    for (int n = 0; n < FN; ++n) {
-        const int row = 16 * (wn * FN + n) + lr;
-        if (row >= ycols) continue;
-#pragma unroll
-        for (int k = 0; k < FK; ++k) {
-            const int col = 16 * (wk * FK + k) + 4 * q;
-            if (col >= xcols) continue;
-            const f32x4 v = acc[n][k];
-            unsigned char* const o = out + kOut * (static_cast<int64_t>(row) * a.K + col);
-            if constexpr (kF32)
-                *reinterpret_cast<f32x4*>(o) = v;
-            else
-                *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         }
     }
 }
@@ -145,14 +224,14 @@ __global__ __launch_bounds__(256) void moe_grouped_dw_join(const float* parts, i
         *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-constexpr int kTile = 128;
+constexpr int kTileN = 128, kTileK = 256;
 
 // Into how many runs the rows of an expert are cut: where the tiles alone do not give
-// every CU two workgroups and there are rows enough for four stages a run.
+// every CU one and there are rows enough for four stages a run.
 int splits_of(int32_t A, int32_t E, int32_t N, int32_t K) {
-    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTile - 1) / kTile) * ((K + kTile - 1) / kTile);
-    const int64_t most = static_cast<int64_t>(A) / E / 256, want = (512 + tiles - 1) / tiles;
-    return static_cast<int>(tiles >= 256 || most < 2 ? 1 : want < most ? want : most);
+    const int64_t tiles = static_cast<int64_t>(E) * ((N + kTileN - 1) / kTileN) * ((K + kTileK - 1) / kTileK);
+    const int64_t most = static_cast<int64_t>(A) / E / 256, want = 256 / tiles;
+    return static_cast<int>(want < 2 || most < 2 ? 1 : want < most ? want : most);
 }
 
 }  // namespace
@@ -163,23 +242,25 @@ size_t grouped_dw_workspace(int32_t A, int32_t E, int32_t N, int32_t K) {
 }
 
 hipError_t launch_grouped_dw(const GroupedGradArgs& a, hipStream_t s) {
-    const uint32_t tn = (a.N + kTile - 1) / kTile, tk = (a.K + kTile - 1) / kTile;
-    const int splits = splits_of(a.A, a.E, a.N, a.K);
-    const int64_t tiles = static_cast<int64_t>(tn) * tk * a.E * splits;
-    const dim3 grid = grid_of((tiles + 7) / 8 * 8), block(256);  // a multiple of 8: the XCDs' shares are rounded up
+    DwTiles t;
+    t.n = (a.N + kTileN - 1) / kTileN;
+    t.k = (a.K + kTileK - 1) / kTileK;
+    t.splits = splits_of(a.A, a.E, a.N, a.K);
+    t.count = t.n * t.k * a.E * t.splits;
+    const dim3 grid(t.count < 256 ? (t.count + 7) / 8 * 8 : 256), block(64 * 12);
     GroupedGradArgs to = a;
-    if (splits > 1) to.dw = a.ws;
-    if (splits > 1 || a.out_f32)
-        hipLaunchKernelGGL((moe_grouped_dw_tile<kTile, kTile, 2, 2, true>), grid, block, 0, s, to, tn, tk, splits);
+    if (t.splits > 1) to.dw = a.ws;
+    if (t.splits > 1 || a.out_f32)
+        hipLaunchKernelGGL((moe_grouped_dw_tile<kTileN, kTileK, 2, 4, 3, true>), grid, block, 0, s, to, t);
     else
-        hipLaunchKernelGGL((moe_grouped_dw_tile<kTile, kTile, 2, 2, false>), grid, block, 0, s, to, tn, tk, splits);
-    if (splits > 1) {
+        hipLaunchKernelGGL((moe_grouped_dw_tile<kTileN, kTileK, 2, 4, 3, false>), grid, block, 0, s, to, t);
+    if (t.splits > 1) {
         const int64_t size = static_cast<int64_t>(a.E) * a.N * a.K;
         const dim3 join = grid_of((size / 4 + 255) / 256);
         if (a.out_f32)
-            hipLaunchKernelGGL((moe_grouped_dw_join<true>), join, block, 0, s, a.ws, size, splits, a.dw);
+            hipLaunchKernelGGL((moe_grouped_dw_join<true>), join, dim3(256), 0, s, a.ws, size, static_cast<int>(t.splits), a.dw);
         else
-            hipLaunchKernelGGL((moe_grouped_dw_join<false>), join, block, 0, s, a.ws, size, splits, a.dw);
+            hipLaunchKernelGGL((moe_grouped_dw_join<false>), join, dim3(256), 0, s, a.ws, size, static_cast<int>(t.splits), a.dw);
     }
     return hipGetLastError();
 }

@@ -372,6 +372,8 @@ struct GroupedArgs {
 hipError_t launch_grouped_bf16(const GroupedArgs& a, hipStream_t stream);
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
 hipError_t launch_grouped_bf16_mx(const GroupedArgs& a, hipStream_t stream);
+bool grouped_few_rows(const GroupedArgs& a);
+hipError_t launch_grouped_few(const GroupedArgs& a, hipStream_t stream);
 
 // The gradient of the experts' weights (grouped_dw.hip).
 struct GroupedGradArgs {

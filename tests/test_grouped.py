@@ -22,7 +22,8 @@ SIZES = [
     ([1], 8, 8), ([0, 3, 0], 64, 64), ([5, 0, 1, 17], 136, 72), ([128], 128, 128), ([129, 0, 127, 1], 264, 200),
     ([16] * 7, 72, 1000), ([300, 2, 65], 1000, 264), ([0, 0, 0], 16, 32), ([1] * 70 + [0] * 60, 40, 96),
     ([3, 0, 0, 1] * 75, 24, 64), ([0] * 1023 + [2], 16, 40), ([1000, 777], 520, 2816), ([40] * 9, 2816, 704),
-    ([2000], 384, 512),
+    ([2000], 384, 512), ([1], 72, 4096), ([3, 0, 16, 1], 200, 1096), ([64], 1000, 1152), ([17, 0, 40], 136, 2056),
+    ([70, 30] * 32, 1408, 1024), ([1, 0] * 32, 1408, 1024),
 ]
 
 
