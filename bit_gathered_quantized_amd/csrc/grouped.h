@@ -74,6 +74,10 @@ __device__ __forceinline__ u32x2 read_turned(const unsigned char* lds, int at) {
     return __builtin_bit_cast(u32x2, v);
 }
 
+// For those reads rows of 2-byte elements lie in pieces of 32 bytes XORed with this: a half
+// wave reads 32 bytes of rows 0 .. 3 and 8 .. 11 (or 4 on) at a time, each from banks of its own.
+__device__ __forceinline__ int turn_key(int row) { return (row & 3) | (row >> 1 & 4); }
+
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }

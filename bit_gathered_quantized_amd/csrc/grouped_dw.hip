@@ -13,12 +13,15 @@ namespace {
 
 using namespace grouped;
 
+// A workgroup takes chunks: neighbouring blocks of columns of dy against one block of x's.  Of an
+// expert of up to D stages the block of x stays in LDS for the whole chunk.
 struct DwTiles {
-    uint32_t n, k, splits, count;  // blocks of columns of dy and of x, runs of an expert's rows, all tiles
+    uint32_t n, k;     // blocks of columns of dy and of x
+    uint32_t chunks;   // of the n blocks
+    uint32_t splits;   // runs of an expert's rows
+    uint32_t count;    // of all chunks
 };
 
-// Pieces of 32 bytes of row r of a stage are XORed with r, for the turning reads: four rows
-// at a time.
 template <int BN, int BK, int WN, int WK, int D, bool kF32>
 __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(GroupedGradArgs a, DwTiles tiles) {
     constexpr int kWaves = WN * WK, kLoaders = 4, FN = BN / WN / 16, FK = BK / WK / 16, kStage = 64;
@@ -33,18 +36,19 @@ __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(Groupe
     if (first >= end) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-    struct Tile {
-        int expert, split, n0, k0, row, rows;  // rows [row, row + rows) of dy and x
+    struct Chunk {
+        int expert, split, n, n_end, k0, row, rows;  // blocks [n, n_end) of dy; rows [row, row + rows) of dy and x
         int stages;
     };
     auto find = [&](uint32_t number) {
-        const uint32_t whole = number / tiles.splits, of_expert = tiles.n * tiles.k;
-        Tile t;
+        const uint32_t whole = number / tiles.splits, of_expert = tiles.chunks * tiles.k;
+        Chunk t;
         t.split = __builtin_amdgcn_readfirstlane(static_cast<int>(number - whole * tiles.splits));
         t.expert = __builtin_amdgcn_readfirstlane(static_cast<int>(whole / of_expert));
-        const uint32_t rest = whole - t.expert * of_expert, kb = rest / tiles.n;
+        const uint32_t rest = whole - t.expert * of_expert, kb = rest / tiles.chunks, chunk = rest - kb * tiles.chunks;
         t.k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(kb * BK));
-        t.n0 = __builtin_amdgcn_readfirstlane(static_cast<int>((rest - kb * tiles.n) * BN));
+        t.n = __builtin_amdgcn_readfirstlane(static_cast<int>(chunk * tiles.n / tiles.chunks));
+        t.n_end = __builtin_amdgcn_readfirstlane(static_cast<int>((chunk + 1) * tiles.n / tiles.chunks));
         int lo = 0, hi = a.A;
         if (a.offsets) {  // through the scalar cache: a vector load would wait for the copies before it
             const auto* const o = (const __attribute__((address_space(4))) int32_t*)a.offsets;
@@ -68,59 +72,74 @@ __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(Groupe
     if (wave >= kWaves) {
         const int w = wave - kWaves;
         uint32_t ahead = first, steps = 0;  // steps: those whose copies are under way
-        Tile t = find(ahead);
-        int stage = 0, buffer = 0;
+        Chunk t = find(ahead);
+        int stage = 0, buffer = 0, x_slot = 0;
+        bool new_x = true, last_x = true;  // whether the stage at hand, and the last issued, copy x
         uint32_t yat[kYJobs], xat[kXJobs];
         int yrow[kYJobs], xrow[kXJobs];
         auto aim = [&] {
-            const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
+            const int ycols = min(BN, a.N - BN * t.n), xcols = min(BK, a.K - t.k0);
 #pragma unroll
             for (int j = 0; j < kYJobs; ++j) {
                 constexpr int kPieces = BN / 8;
                 yrow[j] = 64 / kPieces * (j * kLoaders + w) + lane / kPieces;
-                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (yrow[j] & 7)) + 16 * (p & 1);
+                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ turn_key(yrow[j])) + 16 * (p & 1);
                 yat[j] = col < 2 * ycols ? static_cast<uint32_t>(yrow[j]) * static_cast<uint32_t>(a.dy_stride) + col : kOutside;
             }
 #pragma unroll
             for (int j = 0; j < kXJobs; ++j) {
                 constexpr int kPieces = BK / 8;
                 xrow[j] = 64 / kPieces * (j * kLoaders + w) + lane / kPieces;
-                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ (xrow[j] & 7)) + 16 * (p & 1);
+                const int p = lane % kPieces, col = 32 * ((p >> 1) ^ turn_key(xrow[j])) + 16 * (p & 1);
                 xat[j] = col < 2 * xcols ? static_cast<uint32_t>(xrow[j]) * static_cast<uint32_t>(a.x_stride) + col : kOutside;
             }
         };
         auto issue = [&] {
             // rows past the expert's last read zeros
             const int from = t.row + kStage * stage, rows = min(kStage, t.rows - kStage * stage);
-            const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
-            const Rsrc ry = make_rsrc(static_cast<const unsigned char*>(a.dy) + from * a.dy_stride + 2 * static_cast<int64_t>(t.n0),
+            const int ycols = min(BN, a.N - BN * t.n);
+            const Rsrc ry = make_rsrc(static_cast<const unsigned char*>(a.dy) + from * a.dy_stride + 2 * static_cast<int64_t>(BN * t.n),
                                       static_cast<uint32_t>(max(rows - 1, 0) * a.dy_stride) + 2 * ycols);
-            const Rsrc rx = make_rsrc(static_cast<const unsigned char*>(a.x) + from * a.x_stride + 2 * static_cast<int64_t>(t.k0),
-                                      static_cast<uint32_t>(max(rows - 1, 0) * a.x_stride) + 2 * xcols);
 #pragma unroll
             for (int j = 0; j < kYJobs; ++j)
                 copy16(ry, ybuf[buffer] + 1024 * (j * kLoaders + w), yrow[j] < rows ? yat[j] : kOutside, 0);
+            if (new_x) {
+                const int xcols = min(BK, a.K - t.k0);
+                const Rsrc rx = make_rsrc(static_cast<const unsigned char*>(a.x) + from * a.x_stride + 2 * static_cast<int64_t>(t.k0),
+                                          static_cast<uint32_t>(max(rows - 1, 0) * a.x_stride) + 2 * xcols);
 #pragma unroll
-            for (int j = 0; j < kXJobs; ++j)
-                copy16(rx, xbuf[buffer] + 1024 * (j * kLoaders + w), xrow[j] < rows ? xat[j] : kOutside, 0);
+                for (int j = 0; j < kXJobs; ++j)
+                    copy16(rx, xbuf[x_slot] + 1024 * (j * kLoaders + w), xrow[j] < rows ? xat[j] : kOutside, 0);
+                x_slot = x_slot + 1 == D ? 0 : x_slot + 1;
+            }
+            last_x = new_x;
             buffer = buffer + 1 == D ? 0 : buffer + 1;
             ++steps;
             if (++stage == t.stages) {
                 stage = 0;
-                ahead += step_by;
-                if (ahead < end) {
-                    t = find(ahead);
+                if (++t.n < t.n_end) {
+                    new_x = t.stages > D;
                     aim();
+                } else {
+                    ahead += step_by;
+                    new_x = true;
+                    if (ahead < end) {
+                        t = find(ahead);
+                        aim();
+                    }
                 }
             }
         };
         aim();
         for (int i = 0; i < D - 1 && ahead < end; ++i) issue();
         for (uint32_t at = 0; at < steps; ++at) {
-            if (ahead < end)
+            // all but the last stage's
+            if (ahead >= end)
+                wait_copies<0>();
+            else if (last_x)
                 wait_copies<(D - 2) * kJobs>();
             else
-                wait_copies<0>();
+                wait_copies<(D - 2) * kYJobs>();
             step_barrier();
             if (ahead < end) issue();
         }
@@ -132,36 +151,37 @@ __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(Groupe
     const int r = 8 * q + (lr >> 2);
     int yturn[FN], xturn[FK];
 #pragma unroll
-    for (int n = 0; n < FN; ++n) yturn[n] = r * 2 * BN + 32 * ((wn * FN + n) ^ (r & 7)) + 8 * (lr & 3);
+    for (int n = 0; n < FN; ++n) yturn[n] = r * 2 * BN + 32 * ((wn * FN + n) ^ turn_key(r)) + 8 * (lr & 3);
 #pragma unroll
-    for (int k = 0; k < FK; ++k) xturn[k] = r * 2 * BK + 32 * ((wk * FK + k) ^ (r & 7)) + 8 * (lr & 3);
-    int buffer = 0;
-    for (uint32_t here = first; here < end; here += step_by) {
-        const Tile t = find(here);
-        const int ycols = min(BN, a.N - t.n0), xcols = min(BK, a.K - t.k0);
+    for (int k = 0; k < FK; ++k) xturn[k] = r * 2 * BK + 32 * ((wk * FK + k) ^ turn_key(r)) + 8 * (lr & 3);
+    int buffer = 0, x_base = 0;  // the slot of x's first stage
+    uint32_t here = first;
+    for (Chunk t = find(here);;) {
+        const int n0 = BN * t.n, ycols = min(BN, a.N - n0), xcols = min(BK, a.K - t.k0);
         // whether this wave's part of the tile holds anything
         const bool active = 16 * wn * FN < ycols && 16 * wk * FK < xcols;
 #pragma unroll
         for (int n = 0; n < FN; ++n)
 #pragma unroll
             for (int k = 0; k < FK; ++k) acc[n][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+        int x_now = x_base;
         for (int stage = 0; stage < t.stages; ++stage) {
             step_barrier();
-            const unsigned char *const ys = ybuf[buffer], *const xs = xbuf[buffer];
+            const unsigned char *const ys = ybuf[buffer], *const xs = xbuf[x_now];
             buffer = buffer + 1 == D ? 0 : buffer + 1;
+            x_now = x_now + 1 == D ? 0 : x_now + 1;
             if (!active) continue;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 u32x4 yf[FN], xf[FK];
-                // rows + 4: the XOR turns over bit 2, as that of the piece's number with 4 does
 #pragma unroll
                 for (int n = 0; n < FN; ++n) {
-                    const u32x2 lo = read_turned(ys, yturn[n] + 64 * s * BN), hi = read_turned(ys, (yturn[n] ^ 128) + 64 * s * BN + 8 * BN);
+                    const u32x2 lo = read_turned(ys, yturn[n] + 64 * s * BN), hi = read_turned(ys, yturn[n] + 64 * s * BN + 8 * BN);
                     yf[n] = u32x4{lo[0], lo[1], hi[0], hi[1]};
                 }
 #pragma unroll
                 for (int k = 0; k < FK; ++k) {
-                    const u32x2 lo = read_turned(xs, xturn[k] + 64 * s * BK), hi = read_turned(xs, (xturn[k] ^ 128) + 64 * s * BK + 8 * BK);
+                    const u32x2 lo = read_turned(xs, xturn[k] + 64 * s * BK), hi = read_turned(xs, xturn[k] + 64 * s * BK + 8 * BK);
                     xf[k] = u32x4{lo[0], lo[1], hi[0], hi[1]};
                 }
 #pragma unroll
@@ -176,7 +196,7 @@ __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(Groupe
         // instruction, measured 380 | 343 us at 16384 rows of 128 experts by 1408 x 2816.
         constexpr int kOut = kF32 ? 4 : 2, kBlock = 128 / (16 * kOut);  // products in 128 bytes
         unsigned char* const out = static_cast<unsigned char*>(a.dw) +
-                                   kOut * (((static_cast<int64_t>(t.split) * a.E + t.expert) * a.N + t.n0) * a.K + t.k0);
+                                   kOut * (((static_cast<int64_t>(t.split) * a.E + t.expert) * a.N + n0) * a.K + t.k0);
         const uint32_t pitch = static_cast<uint32_t>(kOut * a.K);
         const Rsrc ro = make_rsrc(out, (ycols - 1) * pitch + kOut * xcols);
         unsigned char* const mine = turn[wave];
@@ -208,6 +228,13 @@ __global__ __launch_bounds__(64 * (WN * WK + 4)) void moe_grouped_dw_tile(Groupe
                 __builtin_amdgcn_wave_barrier();
             }
         }
+        // the next tile reads the same x where it stayed, else the slots that come next
+        const bool same = ++t.n < t.n_end;
+        if (!same || t.stages > D) x_base = x_now;
+        if (same) continue;
+        here += step_by;
+        if (here >= end) break;
+        t = find(here);
     }
 }
 
@@ -246,7 +273,10 @@ hipError_t launch_grouped_dw(const GroupedGradArgs& a, hipStream_t s) {
     t.n = (a.N + kTileN - 1) / kTileN;
     t.k = (a.K + kTileK - 1) / kTileK;
     t.splits = splits_of(a.A, a.E, a.N, a.K);
-    t.count = t.n * t.k * a.E * t.splits;
+    // Chunks of up to three blocks where every CU gets eight, else single ones: 1 | 3 | 4 | 6
+    // blocks at 16384 rows of 128 experts by 1408 x 2816 348 | 294 | 322 | 303 us.
+    t.chunks = static_cast<int64_t>(t.n) * t.k * a.E >= 256 * 8 * 3 ? (t.n + 2) / 3 : t.n;
+    t.count = t.chunks * t.k * a.E * t.splits;
     const dim3 grid(t.count < 256 ? (t.count + 7) / 8 * 8 : 256), block(64 * 12);
     GroupedGradArgs to = a;
     if (t.splits > 1) to.dw = a.ws;

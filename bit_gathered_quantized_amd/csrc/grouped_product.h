@@ -164,7 +164,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
                 const int job = (j - w_jobs) * kCopiers + w;
                 if constexpr (kTurn) {
                     const int pieces = tall ? kLow / 8 : kWide / 8, r = job * (64 / pieces) + lane / pieces, p = lane % pieces;
-                    const int col = 32 * ((p >> 1) ^ (r & 7)) + 16 * (p & 1);
+                    const int col = 32 * ((p >> 1) ^ turn_key(r)) + 16 * (p & 1);
                     return col < 2 * t.cols ? static_cast<uint32_t>(r) * static_cast<uint32_t>(ws) + col : kOutside;
                 } else {
                     const int n = column_of(1024 / kWRow * job + lane / (kWRow / 16));
@@ -291,14 +291,11 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
         const int wm = kLowF ? 0 : tall ? wave >> 1 : wave >> 2, wn = kLowF ? wave : tall ? wave & 1 : wave & 3;
         const int x_rows = tall ? kWide : kLow, columns = tall ? kLow : kWide;
         const int x_from = 64 * wm * kXRow, w_from = x_rows * kXRow + (kTurn ? 0 : kColumns * wn * kWRow);
-        int turned[kTurn ? FN : 1], turned4[kTurn ? FN : 1];  // of columns 16 f of rows 8 q + lr / 4 and 4 on
+        int turned[kTurn ? FN : 1];  // of columns 16 f of row 8 q + lr / 4
         if constexpr (kTurn) {
             const int r = 8 * q + (lr >> 2);
 #pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                turned[f] = w_from + r * 2 * columns + 32 * ((wn * FN + f) ^ (r & 7)) + 8 * (lr & 3);
-                turned4[f] = w_from + (r + 4) * 2 * columns + 32 * ((wn * FN + f) ^ ((r + 4) & 7)) + 8 * (lr & 3);
-            }
+            for (int f = 0; f < FN; ++f) turned[f] = w_from + r * 2 * columns + 32 * ((wn * FN + f) ^ turn_key(r)) + 8 * (lr & 3);
         }
         auto multiply = [&](auto rows_16, const unsigned char* b, const unsigned char* sc) {
             constexpr int M = decltype(rows_16)::value;
@@ -348,7 +345,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
                     if constexpr (kTurn) {
-                        const u32x2 lo = read_turned(b, turned[f] + 64 * S * columns), hi = read_turned(b, turned4[f] + 64 * S * columns);
+                        const u32x2 lo = read_turned(b, turned[f] + 64 * S * columns), hi = read_turned(b, turned[f] + 64 * S * columns + 8 * columns);
                         wf[f] = u32x4{lo[0], lo[1], hi[0], hi[1]};
                     } else {
                         wf[f] = read16(b, w_from + piece + 2048 * f);
