@@ -4,11 +4,11 @@
 namespace moe {
 
 hipError_t launch_grouped_bf16(const GroupedArgs& a, hipStream_t s) {
-    const bool once = read_once(a, 2 * static_cast<int64_t>(a.N) * a.K);
+    const bool once = read_once(a, 2 * static_cast<int64_t>(a.N) * a.K), low = low_strips(a);
     if (a.w_kn)
-        once ? launch_product<Form::kCols, true>(a, s) : launch_product<Form::kCols, false>(a, s);
+        low ? launch_product<Form::kCols, 32>(a, once, s) : launch_product<Form::kCols, 128>(a, once, s);
     else
-        once ? launch_product<Form::kRows, true>(a, s) : launch_product<Form::kRows, false>(a, s);
+        low ? launch_product<Form::kRows, 32>(a, once, s) : launch_product<Form::kRows, 128>(a, once, s);
     return hipGetLastError();
 }
 

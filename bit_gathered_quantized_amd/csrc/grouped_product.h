@@ -7,16 +7,18 @@
 // ahead in the buffer of the last step, and the others multiply.  So neither a tile's end nor the
 // search for the next tile holds up the copies.
 //
-//   kRows       bf16 x, bf16 w [E, N, K]:  a stage is 64 of K
-//   kCols       bf16 x, bf16 w [E, K, N]:  the same, w turned by the reads
-//   kMx         both microscaled:          256 of K
-//   kBf16Mx     bf16 x, microscaled w:     128 of K; strips of 128 rows only
-//   kBf16MxLow  the same, few rows:        256 of K; strips of 64 rows only
+//   kRows    bf16 x, bf16 w [E, N, K]:  a stage is 64 of K
+//   kCols    bf16 x, bf16 w [E, K, N]:  the same, w turned by the reads
+//   kMx      both microscaled:          256 of K
+//   kBf16Mx  bf16 x, microscaled w:     128 of K; no strips of 256 rows
+//
+// For few rows an expert strips have kLow = 32 rows, so that the room of the rows goes to one more
+// buffer, or to stages of 256 of K (kBf16Mx).
 //
 // A buffer holds rows of 128 bytes of K, those of x first, in pieces of 16 bytes XORed
 // with the row's number so that neither the copies nor the reads meet a bank twice (kCols: w
 // as 64 rows of the tile's columns in pieces of 32 bytes; kBf16Mx: rows of 256 bytes of x
-// and 64 of w; kBf16MxLow: of 512 and 128).
+// and 64 of w, or of 512 and 128).
 #pragma once
 
 #include "grouped.h"
@@ -26,7 +28,7 @@ namespace {
 
 using namespace grouped;
 
-enum class Form { kRows, kCols, kMx, kBf16Mx, kBf16MxLow };
+enum class Form { kRows, kCols, kMx, kBf16Mx };
 
 // LDS row r of w holds this column of the tile, so that a lane ends up with 8
 // neighbouring columns of two products.
@@ -95,25 +97,26 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& a, const Tile& t, 
 constexpr int kCopiers = 4, kMultipliers = 8;
 
 // kOnce: w is read once (non-temporal loads).  kShort: K shorter than a stage.
-template <Form F, bool kOnce, bool kF32, bool kShort>
+template <Form F, int kLow, bool kOnce, bool kF32, bool kShort>
 __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_product(GroupedArgs a, uint32_t most) {
-    constexpr bool kLowF = F == Form::kBf16MxLow, kMixed = F == Form::kBf16Mx || kLowF;
-    constexpr bool kMxX = F == Form::kMx, kMxW = kMxX || kMixed, kTurn = F == Form::kCols, kTall = !kMixed;
-    constexpr int kLow = kLowF ? 64 : 128, kWide = 256;              // the tile of a short strip
-    constexpr int BM = kTall ? 2 * kLow : kLow, BN = kWide, D = kLowF ? 2 : 3;
-    constexpr int kStage = kMxX || kLowF ? 256 : F == Form::kBf16Mx ? 128 : 64;  // of K
+    constexpr bool kMxX = F == Form::kMx, kMixed = F == Form::kBf16Mx, kMxW = kMxX || kMixed, kTurn = F == Form::kCols;
+    constexpr bool kLong = kMixed && kLow < 128, kTall = kLow == 128 && !kMixed;
+    constexpr int kWide = 256;                                     // columns of the tile of a short strip
+    constexpr int BM = kTall ? 2 * kLow : kLow, BN = kWide, D = kLow == 128 || kMixed ? 3 : 4;
+    constexpr int kStage = kMxX || kLong ? 256 : kMixed ? 128 : 64;  // of K
     constexpr int kXRow = kMxX ? 128 : 2 * kStage, kWRow = kMxW ? kStage / 2 : 2 * kStage;  // bytes of a row
     constexpr int kBuffer = kLow * kXRow + kWide * kWRow, kJobs = kBuffer / 1024 / kCopiers;
     constexpr int kXJobs = kLow * kXRow / 1024 / kCopiers, kXTall = kTall ? 2 * kXJobs : kXJobs;  // of them x's, in a tall strip
     constexpr int kSB = kStage / 32, kSRows = !kMxW ? 0 : kMxX ? kLow + kWide : kWide;  // scale bytes of a row and stage
     constexpr int kSJobs = (kSRows + 64 * kCopiers - 1) / (64 * kCopiers), kSBuffer = kMxW ? kSRows * kSB : 16;
-    constexpr int FM = 4, FN = kLowF ? 2 : 4, kColumns = 16 * FN;    // a wave's part: 64 rows by kColumns
+    constexpr int FM = kLow == 32 ? 2 : 4, FN = kLow == 128 ? 4 : 2, kColumns = 16 * FN;  // a wave's part: up to 64 rows by kColumns
+    static_assert(kXJobs * kCopiers * 1024 == kLow * kXRow && kJobs * kCopiers * 1024 == kBuffer, "copies");
     static_assert(!kTall || (kXRow == 128 && kWRow == 128 && kWide == 2 * kLow), "a buffer holds either tile");
     __shared__ __align__(16) unsigned char buffers[D][kBuffer];
     __shared__ __align__(16) unsigned char scales[D][kSBuffer];
     __shared__ uint32_t upto[MOE_MAX_EXPERTS];
     // the next tiles, from the copiers to the others: row, rows, n0, cols, flags (1 tall, 2 another follows)
-    constexpr int kTells = 4;  // more than the D tiles between aiming at one and storing it
+    constexpr int kTells = 8;  // more than the D + 1 tiles from the one that is read to the one that is aimed at
     __shared__ __align__(16) int tell[kTells][8];
 
     Share<BM, BN, kTall> share;
@@ -288,7 +291,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
         told = (told + 1) & (kTells - 1);
         more = flags & 2;
         const bool tall = kTall && (flags & 1);
-        const int wm = kLowF ? 0 : tall ? wave >> 1 : wave >> 2, wn = kLowF ? wave : tall ? wave & 1 : wave & 3;
+        const int wm = kLow < 128 ? 0 : tall ? wave >> 1 : wave >> 2, wn = kLow < 128 ? wave : tall ? wave & 1 : wave & 3;
         const int x_rows = tall ? kWide : kLow, columns = tall ? kLow : kWide;
         const int x_from = 64 * wm * kXRow, w_from = x_rows * kXRow + (kTurn ? 0 : kColumns * wn * kWRow);
         int turned[kTurn ? FN : 1];  // of columns 16 f of row 8 q + lr / 4
@@ -300,18 +303,18 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
         auto multiply = [&](auto rows_16, const unsigned char* b, const unsigned char* sc) {
             constexpr int M = decltype(rows_16)::value;
             if constexpr (kMixed) {
-                // lane quarter q holds one block of 128 of K (kBf16MxLow: one of each 128): its
+                // lane quarter q holds one block of 128 of K (kLong: one of each 128): its
                 // 16 bytes of codes become four operands, word i against x's values 8 i .. + 7
                 // of the block (codes under their scale are exact in bf16)
 #pragma unroll
                 for (int s = 0; s < kStage / 128; ++s) {
-                    const int block = kLowF ? 2 * q + s : q;
+                    const int block = kLong ? 2 * q + s : q;
                     u32x4 codes[FN];
                     float unit[FN];
 #pragma unroll
                     for (int f = 0; f < FN; ++f) {
                         const int row = 16 * f + lr;
-                        codes[f] = read16(b, w_from + kWRow * row + 16 * (block ^ (kLowF ? lr & 7 : lr >> 1 & 3)));
+                        codes[f] = read16(b, w_from + kWRow * row + 16 * (block ^ (kLong ? lr & 7 : lr >> 1 & 3)));
                         unit[f] = mx_scale(sc[kSB * (kColumns * wn + row) + block]);
                     }
 #pragma unroll
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
                         u32x4 xf[M];
 #pragma unroll
                         for (int m = 0; m < M; ++m)
-                            xf[m] = read16(b, x_from + kXRow * (16 * m + lr) + 16 * ((4 * block + i) ^ (kLowF ? lr & 7 : lr)));
+                            xf[m] = read16(b, x_from + kXRow * (16 * m + lr) + 16 * ((4 * block + i) ^ (kLong ? lr & 7 : lr)));
 #pragma unroll
                         for (int f = 0; f < FN; ++f) {
                             const u32x4 w = mx_as_bf16(codes[f][i], unit[f]);
@@ -382,7 +385,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
         }
         if (rows_here <= 16)
             run(std::integral_constant<int, 1>());
-        else if (rows_here <= 32)
+        else if (FM == 2 || rows_here <= 32)
             run(std::integral_constant<int, 2>());
         else
             run(std::integral_constant<int, FM>());
@@ -390,19 +393,22 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
     }
 }
 
-template <Form F, bool kOnce>
+template <Form F, int kLow, bool kOnce>
 void launch_product(const GroupedArgs& a, hipStream_t s) {
-    constexpr int kRows = F == Form::kBf16Mx ? 128 : F == Form::kBf16MxLow ? 64 : 256;
-    const int64_t most = most_strips(a, kRows), units = most * ((a.N + kUnit - 1) / kUnit);
+    const int64_t most = most_strips(a, kLow == 128 && F != Form::kBf16Mx ? 256 : kLow), units = most * ((a.N + kUnit - 1) / kUnit);
     const dim3 grid(static_cast<unsigned>(units < 256 ? (units + 7) / 8 * 8 : 256)), block(64 * (kCopiers + kMultipliers));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, static_cast<uint32_t>(most)); };
-    if constexpr (F != Form::kRows && F != Form::kCols) {
-        if (a.K < (F == Form::kBf16Mx ? 128 : 256)) {
-            a.out_f32 ? go(moe_grouped_product<F, kOnce, true, true>) : go(moe_grouped_product<F, kOnce, false, true>);
+    if constexpr (F == Form::kMx || F == Form::kBf16Mx) {
+        if (a.K < (F == Form::kBf16Mx && kLow == 128 ? 128 : 256)) {
+            a.out_f32 ? go(moe_grouped_product<F, kLow, kOnce, true, true>) : go(moe_grouped_product<F, kLow, kOnce, false, true>);
             return;
         }
     }
-    a.out_f32 ? go(moe_grouped_product<F, kOnce, true, false>) : go(moe_grouped_product<F, kOnce, false, false>);
+    a.out_f32 ? go(moe_grouped_product<F, kLow, kOnce, true, false>) : go(moe_grouped_product<F, kLow, kOnce, false, false>);
+}
+template <Form F, int kLow>
+void launch_product(const GroupedArgs& a, bool once, hipStream_t s) {
+    once ? launch_product<F, kLow, true>(a, s) : launch_product<F, kLow, false>(a, s);
 }
 
 // Whether w's rows pass the GPU once and are more than its caches keep (256 MB behind the L2s):
@@ -412,6 +418,11 @@ void launch_product(const GroupedArgs& a, hipStream_t s) {
 inline bool read_once(const GroupedArgs& a, int64_t expert_bytes) {
     return a.A <= 192 * static_cast<int64_t>(a.E) && (a.A < a.E ? a.A : a.E) * expert_bytes > 128 << 20;
 }
+
+// Whether strips of 32 rows are faster, with x and w of one kind.  32 | 128, 128 experts by 1408 x
+// 2816: 64 rows in bf16 68 | 79 us, 1024 rows 169 | 168 us, 4096 rows 213 | 174 us; both
+// microscaled 24 | 26, 49 | 50 and 70 | 58 us.
+inline bool low_strips(const GroupedArgs& a) { return a.A <= 8 * static_cast<int64_t>(a.E); }
 
 }  // namespace
 }  // namespace moe

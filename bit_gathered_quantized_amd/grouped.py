@@ -45,8 +45,8 @@ def _bytes(t, name, dev, shape, other):
     _on(t, name, dev)
     if t.dtype is not _layer.torch.uint8 and t.dtype is not getattr(_layer.torch, other, None):
         raise ValueError(f"{name} must be uint8 or {other}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -260,8 +260,9 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
     width = x.shape[-1]
     if width % (32 if glu is None else 64):
         raise ValueError(f"x has {width} values a row, expected a multiple of {32 if glu is None else 64}")
+    K = width if glu is None else width // 2
     q = MoeMx()
-    q.K, q.type, q.flags = width if glu is None else width // 2, _type(x, "x"), _GLU[glu]
+    q.K, q.type, q.flags = K, _type(x, "x"), _GLU[glu]
     q.R, q.stride = _flat_rows(x, "x", dev, width)
     q.values = x.data_ptr()
     lead = tuple(x.shape[:-1])
@@ -270,11 +271,15 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
     def go(raw):
         c, s = codes, scales
         if c is None:
-            c = _layer.torch.empty(lead + (q.K // 2,), dtype=uint8, device=dev)
-        q.codes = _codes(c, "codes", dev, lead + (q.K // 2,))
+            c = _layer.torch.empty(lead + (K // 2,), dtype=uint8, device=dev)
+            q.codes = c.data_ptr()
+        else:
+            q.codes = _codes(c, "codes", dev, lead + (K // 2,))
         if s is None:
-            s = _layer.torch.empty(lead + (q.K // 32,), dtype=uint8, device=dev)
-        q.scales = _scales(s, "scales", dev, lead + (q.K // 32,))
+            s = _layer.torch.empty(lead + (K // 32,), dtype=uint8, device=dev)
+            q.scales = s.data_ptr()
+        else:
+            q.scales = _scales(s, "scales", dev, lead + (K // 32,))
         st = bgq.lib().moe_mx_quantize(ctypes.byref(q), raw)
         if st != 0:
             raise bgq.MoeError(st, "moe_mx_quantize")
@@ -295,16 +300,18 @@ def mx_dequantize(codes, scales, *, out=None, out_dtype=None, stream=None):
     q = MoeMx()
     q.K = K
     dtype, q.type = _out_type(out, out_dtype)
-    q.codes = _codes(codes, "codes", dev, codes.shape)
+    q.codes = _codes(codes, "codes", dev, lead + (K // 2,))
     q.scales = _scales(scales, "scales", dev, lead + (K // 32,))
 
     def go(raw):
         o = out
         if o is None:
             o = _layer.torch.empty(lead + (K,), dtype=dtype, device=dev)
-        elif tuple(o.shape) != lead + (K,):
-            raise ValueError(f"out has shape {tuple(o.shape)}, expected {lead + (K,)}")
-        q.R, q.stride = _flat_rows(o, "out", dev, K)
+            q.R, q.stride = o.numel() // max(K, 1), K
+        else:
+            if o.shape != lead + (K,):
+                raise ValueError(f"out has shape {tuple(o.shape)}, expected {lead + (K,)}")
+            q.R, q.stride = _flat_rows(o, "out", dev, K)
         q.values = o.data_ptr()
         st = bgq.lib().moe_mx_dequantize(ctypes.byref(q), raw)
         if st != 0:
