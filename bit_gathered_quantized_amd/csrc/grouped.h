@@ -27,28 +27,14 @@ template <bool kOnce = false>
 __device__ __forceinline__ void copy16(Rsrc r, unsigned char* lds, uint32_t at, uint32_t step) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsByte*)lds, 16, at, step, 0, kOnce ? 2 : 0);
 }
-// The wave's copies but the last n are in LDS; then those of all waves, and every
-// wave is done with what it read before.
-template <int N>
-__device__ __forceinline__ void copies_done() {
-    static_assert(N < 64, "vmcnt");
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);  // the other counters are not waited for
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-}
-
-// Of a wave that only copies: all but its last n are in LDS.  (Where n is not known at
-// compile time: none.)
+// Of a wave that only copies: all but its last N copies are in LDS.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
     static_assert(N < 64, "vmcnt");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
 }
-// Barrier of all waves; what they wrote to LDS before it is waited for by themselves.
+// Barrier of all waves; each has waited for its own writes to LDS and copies before.
 __device__ __forceinline__ void step_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -62,9 +48,6 @@ __device__ __forceinline__ u32x4 read16(const unsigned char* lds, int at) {
 }
 __device__ __forceinline__ void store16(Rsrc r, u32x4 v, uint32_t at) {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
-}
-__device__ __forceinline__ void store8(Rsrc r, u32x2 v, uint32_t at) {
-    __builtin_amdgcn_raw_buffer_store_b64(v, r, at, 0, 0);
 }
 // Four rows of 16 columns (2-byte elements): lane 4 r + c of each 16 points at columns
 // 4 c .. 4 c + 3 of row r and gets column l of the four rows, l its number in the 16.

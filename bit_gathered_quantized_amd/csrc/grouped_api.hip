@@ -25,9 +25,9 @@ moe_status check(const moe_grouped* g) {
         return MOE_ERR_UNSUPPORTED;
     const moe_status st = check_sizes(g->A, g->E, g->N, g->K, wm ? 32 : 8);
     if (st != MOE_OK) return st;
-    // strips of 128 rows by units of 32 columns: the kernels' sums over them stay within 32 bits
-    // (smaller strips are for few rows)
-    if ((static_cast<int64_t>(g->A) / 128 + g->E) * ((g->N + 31) / 32) >= 1 << 24) return MOE_ERR_SHAPE;
+    // strips of rows by units of 32 columns: the kernels' sums over them stay within 32 bits
+    const int64_t strip = g->A <= moe::kGroupedLowRows * static_cast<int64_t>(g->E) ? 32 : 128;
+    if ((g->A / strip + g->E) * ((g->N + 31) / 32) >= 1 << 24) return MOE_ERR_SHAPE;
     if (!xm && !input_stride(g->x_stride)) return MOE_ERR_SHAPE;
     if (!wm && (!input_stride(g->w_stride) || g->w_expert_stride < 0 || g->w_expert_stride % 8)) return MOE_ERR_SHAPE;
     if (g->out_stride < g->N || g->out_stride > MOE_GROUPED_MAX_STRIDE || g->out_stride % (g->out_type == MOE_T_FP32 ? 4 : 8))

@@ -369,6 +369,7 @@ struct GroupedArgs {
     void* out;
     int64_t x_stride, w_stride, w_expert, out_stride;  // bytes
 };
+constexpr int kGroupedLowRows = 192;  // more rows an expert on average: no strips of 32 rows
 hipError_t launch_grouped_bf16(const GroupedArgs& a, hipStream_t stream);
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t stream);
 hipError_t launch_grouped_bf16_mx(const GroupedArgs& a, hipStream_t stream);

@@ -486,18 +486,22 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
  *
  * The second form is the gradient of the rows: with dy [A, N] and the forward's w
  * [E, N, K] it gives dx [A, K].  Products are exact, sums fp32, out is rounded once.
- * A row's result depends on that row and its expert alone.  Rows outside
- * [offsets[0], offsets[E]) are not written.
+ * Rows outside [offsets[0], offsets[E]) are not written.  A row's result depends on
+ * that row and its expert alone (its last bits on the sizes A, E, N and K as well).
  *
  * x and w are bf16, or microscaled 4-bit values: both, or w alone.  Microscaled rows
  * are the codes [.., K / 2] and scales [.., K / 32] of moe_mx_quantize, contiguous; they
- * do not go with MOE_G_W_KN (the scales lie along K).
+ * do not go with MOE_G_W_KN (the scales lie along K).  Scale bytes from elsewhere may be
+ * any; against bf16 rows a value of w past bf16's range (scale bytes 253 and 254) counts
+ * as infinity.
  */
 #define MOE_G_W_KN 1u
 #define MOE_GROUPED_MAX_STRIDE (1 << 22)
 #define MOE_GROUPED_MAX_DIM (1 << 20)
 typedef struct {
-    int32_t A;                 /* rows, 0 <= A < 2^30                                  */
+    int32_t A;                 /* rows, 0 <= A < 2^30; (A / 128 + E) (N / 32) < 2^24,
+                                  with up to 192 rows an expert (A / 32 + E) (N / 32)
+                                  (else MOE_ERR_SHAPE)                                 */
     int32_t E;                 /* experts, 1 <= E <= MOE_MAX_EXPERTS                   */
     int32_t N;                 /* columns of out: a multiple of 8, <= MOE_GROUPED_MAX_DIM */
     int32_t K;                 /* length of a sum: a multiple of 8 (microscaled w: of

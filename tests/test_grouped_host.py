@@ -31,7 +31,7 @@ MX2 = dict(MX, x_type=2, x_scales=6 * P)
     (dict(x_stride=-8), -2), (dict(x_stride=100), -2), (dict(x_stride=(1 << 22) + 8), -2), (dict(w_stride=-8), -2),
     (dict(w_stride=97), -2), (dict(w_expert_stride=-8), -2), (dict(w_expert_stride=100), -2), (dict(out_stride=63), -2),
     (dict(out_stride=56), -2), (dict(out_stride=68), -2), (dict(out_type=1, out_stride=66), -2),
-    (dict(A=(1 << 30) - 1, N=1 << 20), -2),
+    (dict(A=(1 << 30) - 1, N=1 << 20), -2), (dict(A=20000, E=512, N=1 << 20), -2), (dict(MX, A=190 * 512, E=512, N=1 << 18, K=32), -2),
     (dict(x=None), -1), (dict(w=None), -1), (dict(out=None), -1), (dict(offsets=None), -1), (dict(MX, w_scales=None), -1),
     (dict(MX2, x_scales=None), -1),
     (dict(x=2 * P + 8), -4), (dict(w=3 * P + 2), -4), (dict(out=4 * P + 4), -4), (dict(offsets=P + 2), -4),
