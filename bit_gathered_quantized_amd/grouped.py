@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 
 from . import layer as _layer
-from .layer import MOE_T_BF16, MOE_T_FP32, _call, _device, _new_or_given, _on, _rows, _type
+from .layer import MOE_T_BF16, MOE_T_FP32, _call, _device, _output, _on, _rows, _type
 
 __all__ = ["MoeGrouped", "MoeGroupedGrad", "MoeMx", "grouped_matmul", "grouped_matmul_dw", "grouped_dw_workspace_bytes",
            "mx_quantize", "mx_dequantize", "MOE_T_MXFP4", "MOE_G_W_KN", "MOE_Q_GELU", "MOE_Q_SILU"]
@@ -43,8 +43,9 @@ class MoeMx(ctypes.Structure):
 def _bytes(t, name, dev, shape, other):
     """Data pointer of contiguous codes or scales: uint8, or the type `other` of torch that holds the same bytes."""
     _on(t, name, dev)
-    if t.dtype is not _layer.torch.uint8 and t.dtype is not getattr(_layer.torch, other, None):
-        raise ValueError(f"{name} must be uint8 or {other}, got {t.dtype}")
+    dtype = t.dtype
+    if dtype is not _layer.torch.uint8 and dtype is not getattr(_layer.torch, other, None):
+        raise ValueError(f"{name} must be uint8 or {other}, got {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if not t.is_contiguous():
@@ -109,58 +110,56 @@ def grouped_matmul(x, w, offsets=None, *, x_scales=None, w_scales=None, transpos
     that belong to no expert are not written.  Returns out."""
     bgq = _layer._api()
     dev = _device(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [A, K]")
-    if w.dim() != 3 and (w.dim() != 2 or offsets is not None):
-        raise ValueError(f"w has shape {tuple(w.shape)}, expected {'[E, N, K]' if offsets is not None else '[N, K]'}")
-    if w.dim() == 2:
-        w = w.unsqueeze(0)
+    xshape, shape = tuple(x.shape), tuple(w.shape)
+    if len(xshape) != 2:
+        raise ValueError(f"x has shape {xshape}, expected [A, K]")
+    if len(shape) != 3 and (len(shape) != 2 or offsets is not None):
+        raise ValueError(f"w has shape {shape}, expected {'[E, N, K]' if offsets is not None else '[N, K]'}")
+    if len(shape) == 2:
+        w, shape = w.unsqueeze(0), (1,) + shape
         w_scales = None if w_scales is None else w_scales.unsqueeze(0)
-    E, A = w.shape[0], x.shape[0]
+    (E, N, K), A = shape, xshape[0]
     if offsets is None and E != 1:
         raise ValueError(f"w holds {E} experts: offsets are needed")
     _rows_count(A, "x")
-    g = MoeGrouped()
-    g.A, g.E = A, E
-    dtype, g.out_type = _out_type(out, out_dtype)
+    dtype, out_type = _out_type(out, out_dtype)
+    w_type = x_type = MOE_T_BF16
+    flags = w_stride = w_expert = x_stride = 0
+    ws = xs = None
     if w_scales is not None:
         if transpose:
             raise ValueError("microscaled weights cannot be transposed: their scales lie along K")
-        N, K = w.shape[1], 2 * w.shape[2]
-        g.w_type = MOE_T_MXFP4
-        g.w = _codes(w, "w", dev, (E, N, K // 2))
-        g.w_scales = _scales(w_scales, "w_scales", dev, (E, N, K // 32))
+        K, w_type = 2 * K, MOE_T_MXFP4
+        wp, ws = _codes(w, "w", dev, shape), _scales(w_scales, "w_scales", dev, (E, N, K // 32))
     else:
-        N, K = (w.shape[2], w.shape[1]) if transpose else (w.shape[1], w.shape[2])
         _on(w, "w", dev)
         _bf16(w, "w")
-        if w.stride(2) != 1 and w.shape[2] > 1:
+        w_expert, w_stride, one = w.stride()
+        if one != 1 and K > 1:
             raise ValueError("w must be contiguous along its rows")
-        g.flags = MOE_G_W_KN if transpose else 0
-        g.w = w.data_ptr()
-        g.w_stride = w.stride(1) if w.shape[1] > 1 else w.shape[2]
-        g.w_expert_stride = w.stride(0) if E > 1 else 0
+        if N == 1:
+            w_stride = K
+        if E == 1:
+            w_expert = 0
+        if transpose:
+            N, K, flags = K, N, MOE_G_W_KN
+        wp = w.data_ptr()
     if x_scales is not None:
         if w_scales is None:
             raise ValueError("x_scales are given without w_scales")
-        g.x_type = MOE_T_MXFP4
-        g.x = _codes(x, "x", dev, (A, K // 2))
-        g.x_scales = _scales(x_scales, "x_scales", dev, (A, K // 32))
+        x_type = MOE_T_MXFP4
+        xp, xs = _codes(x, "x", dev, (A, K // 2)), _scales(x_scales, "x_scales", dev, (A, K // 32))
     else:
         _bf16(x, "x")
-        g.x_stride, g.x = _rows(x, "x", dev, A, K), x.data_ptr()
-    g.N, g.K = N, K
-    if offsets is not None:
-        g.offsets = _offsets(offsets, dev, E)
+        x_stride, xp = _rows(x, "x", dev, A, K), x.data_ptr()
+    op = None if offsets is None else _offsets(offsets, dev, E)
 
     def go(raw):
-        o = out
-        if o is None:
-            o = _layer.torch.empty((A, N), dtype=dtype, device=dev)
-            g.out_stride = N
+        if out is None:
+            o, stride = _layer.torch.empty(A, N, dtype=dtype, device=dev), N
         else:
-            g.out_stride = _rows(o, "out", dev, A, N)
-        g.out = o.data_ptr()
+            o, stride = out, _rows(out, "out", dev, A, N)
+        g = MoeGrouped(A, E, N, K, x_type, w_type, out_type, flags, op, xp, wp, xs, ws, o.data_ptr(), x_stride, w_stride, w_expert, stride)
         st = bgq.lib().moe_grouped_matmul(ctypes.byref(g), raw)
         if st != 0:
             raise bgq.MoeError(st, "moe_grouped_matmul")
@@ -186,23 +185,25 @@ def grouped_matmul_dw(dy, x, offsets=None, *, out=None, out_dtype=None, workspac
     E, N, K) bytes, one per call at a time (allocated if None).  Returns out."""
     bgq = _layer._api()
     dev = _device(dy, "dy")
-    if dy.dim() != 2 or x.dim() != 2:
-        raise ValueError(f"dy and x must be [A, N] and [A, K], got {tuple(dy.shape)} and {tuple(x.shape)}")
-    (A, N), K = dy.shape, x.shape[1]
+    shape, xshape = tuple(dy.shape), tuple(x.shape)
+    if len(shape) != 2 or len(xshape) != 2:
+        raise ValueError(f"dy and x must be [A, N] and [A, K], got {shape} and {xshape}")
+    (A, N), K = shape, xshape[1]
     _rows_count(A, "dy")
-    E = 1 if offsets is None else offsets.shape[0] - 1
-    g = MoeGroupedGrad()
-    g.A, g.E, g.N, g.K = A, E, N, K
-    dtype, g.out_type = _out_type(out, out_dtype)
+    E = 1 if offsets is None else offsets.numel() - 1
+    dtype, out_type = _out_type(out, out_dtype)
     _bf16(dy, "dy")
     _bf16(x, "x")
-    g.dy_stride, g.dy = _rows(dy, "dy", dev, A, N), dy.data_ptr()
-    g.x_stride, g.x = _rows(x, "x", dev, A, K), x.data_ptr()
-    if offsets is not None:
-        g.offsets = _offsets(offsets, dev, E)
+    dy_stride, x_stride = _rows(dy, "dy", dev, A, N), _rows(x, "x", dev, A, K)
+    op = None if offsets is None else _offsets(offsets, dev, E)
+    g = MoeGroupedGrad(A, E, N, K, out_type, op, dy.data_ptr(), x.data_ptr(), None, dy_stride, x_stride)
 
     def go(raw):
-        o, g.dw = _new_or_given(out, "out", dev, (E, N, K), dtype)
+        if out is None:
+            o = _layer.torch.empty(E, N, K, dtype=dtype, device=dev)
+            g.dw = o.data_ptr()
+        else:
+            o, g.dw = out, _output(out, "out", dev, (E, N, K), dtype)
         ws = workspace
         if ws is None:
             need = bgq.lib().moe_grouped_dw_workspace_bytes(ctypes.byref(g))
@@ -221,15 +222,18 @@ def grouped_matmul_dw(dy, x, offsets=None, *, out=None, out_dtype=None, workspac
     return _call(dev, stream, go)
 
 
-def _flat_rows(t, name, dev, width):
-    """(rows, row stride) of a tensor whose last dimension is `width`: strided in two dimensions, contiguous in more."""
-    _on(t, name, dev)
-    if t.dim() == 2:
-        return t.shape[0], _rows(t, name, dev, t.shape[0], width)
+def _flat_rows(t, name, shape, width):
+    """(rows, row stride) of a tensor of that shape whose last dimension is `width`: strided in two dimensions,
+    contiguous in more."""
+    rows = shape[0]
+    if len(shape) == 2:
+        row, one = t.stride()
+        if one != 1 and width > 1:
+            raise ValueError(f"{name} must be contiguous along its rows")
+        return rows, row if rows > 1 else max(width, 1)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (or two-dimensional with contiguous rows)")
-    rows = 1
-    for n in t.shape[:-1]:
+    for n in shape[1:-1]:
         rows *= n
     return rows, width
 
@@ -253,30 +257,29 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
     grouped_matmul takes them."""
     bgq = _layer._api()
     dev = _device(x, "x")
-    if x.dim() < 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., K]")
+    shape = tuple(x.shape)
+    if len(shape) < 2:
+        raise ValueError(f"x has shape {shape}, expected [..., K]")
     if glu not in _GLU:
         raise ValueError(f"glu must be None, 'gelu' or 'silu', got {glu!r}")
-    width = x.shape[-1]
+    width = shape[-1]
     if width % (32 if glu is None else 64):
         raise ValueError(f"x has {width} values a row, expected a multiple of {32 if glu is None else 64}")
     K = width if glu is None else width // 2
-    q = MoeMx()
-    q.K, q.type, q.flags = K, _type(x, "x"), _GLU[glu]
-    q.R, q.stride = _flat_rows(x, "x", dev, width)
-    q.values = x.data_ptr()
-    lead = tuple(x.shape[:-1])
+    rows, stride = _flat_rows(x, "x", shape, width)
+    q = MoeMx(rows, K, _type(x, "x"), _GLU[glu], x.data_ptr(), None, None, stride)
+    lead = shape[:-1]
     uint8 = _layer.torch.uint8
 
     def go(raw):
         c, s = codes, scales
         if c is None:
-            c = _layer.torch.empty(lead + (K // 2,), dtype=uint8, device=dev)
+            c = _layer.torch.empty(*lead, K // 2, dtype=uint8, device=dev)
             q.codes = c.data_ptr()
         else:
             q.codes = _codes(c, "codes", dev, lead + (K // 2,))
         if s is None:
-            s = _layer.torch.empty(lead + (K // 32,), dtype=uint8, device=dev)
+            s = _layer.torch.empty(*lead, K // 32, dtype=uint8, device=dev)
             q.scales = s.data_ptr()
         else:
             q.scales = _scales(s, "scales", dev, lead + (K // 32,))
@@ -294,24 +297,23 @@ def mx_dequantize(codes, scales, *, out=None, out_dtype=None, stream=None):
     exactly)."""
     bgq = _layer._api()
     dev = _device(codes, "codes")
-    if codes.dim() < 2:
-        raise ValueError(f"codes have shape {tuple(codes.shape)}, expected [..., K / 2]")
-    lead, K = tuple(codes.shape[:-1]), 2 * codes.shape[-1]
-    q = MoeMx()
-    q.K = K
-    dtype, q.type = _out_type(out, out_dtype)
-    q.codes = _codes(codes, "codes", dev, lead + (K // 2,))
-    q.scales = _scales(scales, "scales", dev, lead + (K // 32,))
+    shape = tuple(codes.shape)
+    if len(shape) < 2:
+        raise ValueError(f"codes have shape {shape}, expected [..., K / 2]")
+    lead, K = shape[:-1], 2 * shape[-1]
+    dtype, kind = _out_type(out, out_dtype)
+    q = MoeMx(0, K, kind, 0, None, _codes(codes, "codes", dev, shape), _scales(scales, "scales", dev, lead + (K // 32,)), 0)
 
     def go(raw):
         o = out
         if o is None:
-            o = _layer.torch.empty(lead + (K,), dtype=dtype, device=dev)
+            o = _layer.torch.empty(*lead, K, dtype=dtype, device=dev)
             q.R, q.stride = o.numel() // max(K, 1), K
         else:
+            _on(o, "out", dev)
             if o.shape != lead + (K,):
                 raise ValueError(f"out has shape {tuple(o.shape)}, expected {lead + (K,)}")
-            q.R, q.stride = _flat_rows(o, "out", dev, K)
+            q.R, q.stride = _flat_rows(o, "out", lead + (K,), K)
         q.values = o.data_ptr()
         st = bgq.lib().moe_mx_dequantize(ctypes.byref(q), raw)
         if st != 0:

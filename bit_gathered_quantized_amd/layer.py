@@ -112,7 +112,7 @@ def _ambient(dev, stream):
 
 def _call(dev, stream, f):
     """f(raw stream) with the device and stream current; no context in the usual case."""
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev.index == torch._C._cuda_getDevice():  # current_device() without its check: a tensor is there
         return f(torch._C._cuda_getCurrentRawStream(dev.index))  # current_stream() without its object
     with _ambient(dev, stream):
         return f(torch.cuda.current_stream(dev).cuda_stream)
