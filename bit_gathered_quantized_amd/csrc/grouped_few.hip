@@ -3,15 +3,16 @@
 
 namespace moe {
 
-// Few rows an expert and not many weights: then a call is bound by latency, and streams
-// of its own for every 16 columns and eighth of K are faster than tiles that step through K.
-// Few | tiles: 1 row of 4096 x 4096 in bf16 9.4 | 29 us, 8 rows of 8 of 128 experts by 1408 x
-// 2816 15 | 22 us (codes, bf16 rows 9.8 | 15 us); where reading the weights takes long the
-// tiles read them faster (64 rows of 51 of these experts, 405 MB, 95 | 79 us), and for a short
-// K they have few steps (8 rows, K 704, N 2816, 12 | 11 us).
+// Few rows an expert, and workgroups of 64 columns for about one round: then a call is bound by
+// latency, and streams of its own for every 16 columns and eighth of K are faster than tiles that
+// step through K.  Few | tiles, us: 1 row of 4096 x 4096 in bf16 9.2 | 29; 8 rows of 8 experts by 1408 x
+// 2816 (176 workgroups) 15 | 22, codes with bf16 rows 9.8 | 13.6, both as codes 8.9 | 11.0; 12 such
+// experts (264) 15 | 22; 64 rows of 1 expert by 4096 x 4096 (320) 22 | 30.  More workgroups: 8
+// experts by 4096 x 2816 (512) 37 | 34, codes of 4096 x 4096 with bf16 rows 23 | 17; 64 rows by 8192
+// x 4096 (640) 41 | 31; 64 experts by 1408 x 2816 (1408) 90 | 70.  For a shorter K the tiles have few
+// steps (8 rows, K 704, N 2816, 12 | 11).
 bool grouped_few_rows(const GroupedArgs& a) {
-    const int64_t row = a.ws ? a.K / 2 : 2 * static_cast<int64_t>(a.K), touched = (a.A < a.E ? a.A : a.E) * a.N * row;
-    return !a.w_kn && a.K >= 1024 && (a.A <= 64 || a.A <= 4 * static_cast<int64_t>(a.E)) && touched <= 80 << 20;
+    return !a.w_kn && a.K >= 1024 && (a.A <= 64 || a.A <= 4 * static_cast<int64_t>(a.E)) && most_strips(a, 16) * ((a.N + 63) / 64) <= 320;
 }
 
 hipError_t launch_grouped_few(const GroupedArgs& a, hipStream_t s) {

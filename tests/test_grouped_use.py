@@ -278,6 +278,17 @@ def test_scales_at_the_ends(sizes, N, K):
     check(got[~nan], ref[~nan], size[~nan], K)
 
 
+# few rows: wide columns of workgroups (more than 512 narrow ones), their last one in part
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("form", ["bf16", "mx", "bf16 mx"])
+@pytest.mark.parametrize("sizes,N,K", [([1] * 8, 1408, 1024), ([64], 4040, 1152), ([3, 0, 17, 1], 2504, 1056), ([0, 2], 4096, 2080)])
+def test_few_rows(sizes, N, K, form, out):
+    g = gen(N + K)
+    args, kw, x, w = operands(form, g, sum(sizes), len(sizes), N, K)
+    offsets = offsets_of(sizes)
+    check(bgq.grouped_matmul(*args, offsets, out_dtype=out, **kw), *product(x, w, offsets), K)
+
+
 @pytest.mark.parametrize("sizes,K", [([3, 0, 2], 64), ([300, 70], 128), ([2, 1], 1024)])
 def test_codes_past_bf16(sizes, K):
     """Against bf16 rows 6 * 2^127 counts as infinity, 1.5 * 2^126 as itself."""
