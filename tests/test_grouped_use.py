@@ -406,3 +406,69 @@ def test_codes_past_32_bits():
     x[R - 1] = 7.0
     bgq.mx_dequantize(codes, scales, out=x)
     assert torch.equal(x[R - 1].to(F64), decode(codes[R - 1], scales[R - 1]))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("A,N,K", [(1, 1 << 20, 32), (2, 16, 1 << 20), (40, 8, 1 << 18)])
+def test_longest_dimensions(form, A, N, K):
+    g = gen(A)
+    args, kw, x, w = operands(form, g, A, 1, N, K)
+    for starts in (None, offsets_of([A])):
+        check(bgq.grouped_matmul(*args, starts, out_dtype=F32, **kw), *product(x, w, offsets_of([A])), K)
+
+
+@pytest.mark.parametrize("A,N,K", [(3, 1 << 20, 8), (3, 8, 1 << 20), (70, 8, 1 << 17)])
+def test_longest_dimensions_of_a_gradient(A, N, K):
+    g = gen(N)
+    dy, x = normal(g, A, N), normal(g, A, K)
+    check(bgq.grouped_matmul_dw(dy, x), *gradient(dy, x, offsets_of([A])), A)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_millions_of_rows(form):
+    g = gen(11)
+    sizes, N, K = [1, 0, 2000003, 900000], 8, 32
+    args, kw, x, w = operands(form, g, sum(sizes), len(sizes), N, K)
+    offsets = offsets_of(sizes)
+    check(bgq.grouped_matmul(*args, offsets, **kw), *product(x, w, offsets), K)
+
+
+def test_a_gradient_of_millions_of_rows():
+    g = gen(12)
+    sizes = [1, 0, 2000003, 900000]
+    dy, x, offsets = normal(g, sum(sizes), 8), normal(g, sum(sizes), 16), offsets_of(sizes)
+    assert bgq.grouped_dw_workspace_bytes(sum(sizes), 4, 8, 16) > 0
+    check(bgq.grouped_matmul_dw(dy, x, offsets, out_dtype=F32), *gradient(dy, x, offsets), max(sizes))
+
+
+@pytest.mark.parametrize("A,N,K", [(1, 72, 1024), (33, 200, 1056), (50, 2504, 1120)])
+def test_few_rows_of_one_matrix(A, N, K):
+    """Without offsets, rows strided, fp32 rows of out on 16 bytes alone."""
+    g = gen(A)
+    wide = torch.full((A, K + 40), torch.nan, dtype=BF, device="cuda")
+    x = wide[:, 8:8 + K]
+    x.copy_(normal(g, A, K))
+    w = normal(g, N, K)
+    wc, ws = random_mx(g, N, K)
+    xc, xs = random_mx(g, A, K)
+    out = torch.full((A, N + 12), 3.0, dtype=F32, device="cuda")
+    for args, kw, xv, wv in (((x, w), {}, x, w), ((x, wc), dict(w_scales=ws), x, decode(wc, ws)),
+                             ((xc, wc), dict(x_scales=xs, w_scales=ws), decode(xc, xs), decode(wc, ws))):
+        bgq.grouped_matmul(*args, out=out[:, 4:4 + N], **kw)
+        check(out[:, 4:4 + N], *product(xv, wv[None], offsets_of([A])), K)
+        assert bool((out[:, :4] == 3).all()) and bool((out[:, 4 + N:] == 3).all())
+
+
+def test_strided_rows_with_codes():
+    g = gen(13)
+    sizes, N, K = [200, 3], 136, 416
+    x = torch.full((203, K + 16), torch.nan, dtype=BF, device="cuda")[:, 8:8 + K]
+    x.copy_(normal(g, 203, K))
+    wc, ws = random_mx(g, 2, N, K)
+    offsets, one = offsets_of(sizes), x[:1].expand(203, K)
+    check(bgq.grouped_matmul(x, wc, offsets, w_scales=ws), *product(x, decode(wc, ws), offsets), K)
+    check(bgq.grouped_matmul(one, wc, offsets, w_scales=ws), *product(one, decode(wc, ws), offsets), K)
+    w = normal(g, 2, 1, K).expand(2, N, K)  # rows of w all the same, stride 0
+    check(bgq.grouped_matmul(x, w, offsets), *product(x, w, offsets), K)
+    dy = normal(g, 1, N).expand(203, N)
+    check(bgq.grouped_matmul_dw(dy, x, offsets), *gradient(dy, x, offsets), 200)
