@@ -5,7 +5,10 @@ namespace moe {
 
 hipError_t launch_grouped_mx(const GroupedArgs& a, hipStream_t s) {
     const bool once = read_once(a, static_cast<int64_t>(a.N) * a.K / 2);
-    low_strips(a) ? launch_product<Form::kMx, 32>(a, once, s) : launch_product<Form::kMx, 128>(a, once, s);
+    if (big_tiles(a))
+        launch_product<Form::kMx, 256, false>(a, s);
+    else
+        low_strips(a) ? launch_product<Form::kMx, 32>(a, once, s) : launch_product<Form::kMx, 128>(a, once, s);
     return hipGetLastError();
 }
 

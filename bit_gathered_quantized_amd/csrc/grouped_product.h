@@ -12,6 +12,9 @@
 //   kMx      both microscaled:          256 of K
 //   kBf16Mx  bf16 x, microscaled w:     128 of K; no strips of 256 rows
 //
+// For many rows an expert there are tiles of 256 x 256 (kLow = 256), a wave's part 64 by 128, with two
+// buffers: a third less to copy and a quarter less to read from LDS for a product.
+//
 // For few rows an expert strips have kLow = 32 rows, so that the room of the rows goes to one more
 // buffer, or to stages of 256 of K (kBf16Mx).
 //
@@ -19,8 +22,8 @@
 // 180 us for 1.05 GB) and, from 32 rows an expert on, the way from L2 to LDS, since each block of columns
 // brings the strip's rows again (16384 rows of 128 experts by 1408 x 2816: 255 us for 1.15 GB of
 // memory and 1.9 GB of copies; both sides microscaled 88 us); with few experts the rate at which LDS
-// feeds the products (16381 rows of 8 experts by 2816 x 4096: 345 us, 1100 TFLOP/s; microscaled 138 us,
-// 2700 TFLOP/s, where reads and copies take as many cycles of LDS as the products take).
+// feeds the products (16381 rows of 8 experts by 2816 x 4096: 337 us, 1120 TFLOP/s; microscaled 121 us,
+// 3120 TFLOP/s; a stage's reads and copies take as many cycles of LDS as its products on the matrix units).
 //
 // A buffer holds rows of 128 bytes of K, those of x first, in pieces of 16 bytes XORed
 // with the row's number so that neither the copies nor the reads meet a bank twice (kCols: w
@@ -107,16 +110,16 @@ constexpr int kCopiers = 4, kMultipliers = 8;
 template <Form F, int kLow, bool kOnce, bool kF32, bool kShort>
 __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_product(GroupedArgs a, uint32_t most) {
     constexpr bool kMxX = F == Form::kMx, kMixed = F == Form::kBf16Mx, kMxW = kMxX || kMixed, kTurn = F == Form::kCols;
-    constexpr bool kLong = kMixed && kLow < 128, kTall = kLow == 128 && !kMixed;
+    constexpr bool kLong = kMixed && kLow < 128, kTall = kLow == 128 && !kMixed, kBig = kLow == 256;
     constexpr int kWide = 256;                                     // columns of the tile of a short strip
-    constexpr int BM = kTall ? 2 * kLow : kLow, BN = kWide, D = kLow == 128 || kMixed ? 3 : 4;
+    constexpr int BM = kTall ? 2 * kLow : kLow, BN = kWide, D = kBig ? 2 : kLow == 128 || kMixed ? 3 : 4;
     constexpr int kStage = kMxX || kLong ? 256 : kMixed ? 128 : 64;  // of K
     constexpr int kXRow = kMxX ? 128 : 2 * kStage, kWRow = kMxW ? kStage / 2 : 2 * kStage;  // bytes of a row
     constexpr int kBuffer = kLow * kXRow + kWide * kWRow, kJobs = kBuffer / 1024 / kCopiers;
     constexpr int kXJobs = kLow * kXRow / 1024 / kCopiers, kXTall = kTall ? 2 * kXJobs : kXJobs;  // of them x's, in a tall strip
     constexpr int kSB = kStage / 32, kSRows = !kMxW ? 0 : kMxX ? kLow + kWide : kWide;  // scale bytes of a row and stage
     constexpr int kSJobs = (kSRows + 64 * kCopiers - 1) / (64 * kCopiers), kSBuffer = kMxW ? kSRows * kSB : 16;
-    constexpr int FM = kLow == 32 ? 2 : 4, FN = kLow == 128 ? 4 : 2, kColumns = 16 * FN;  // a wave's part: up to 64 rows by kColumns
+    constexpr int FM = kLow == 32 ? 2 : 4, FN = kBig ? 8 : kLow == 128 ? 4 : 2, kColumns = 16 * FN;  // a wave's part: up to 64 rows by kColumns
     static_assert(kXJobs * kCopiers * 1024 == kLow * kXRow && kJobs * kCopiers * 1024 == kBuffer, "copies");
     static_assert(!kTall || (kXRow == 128 && kWRow == 128 && kWide == 2 * kLow), "a buffer holds either tile");
     __shared__ __align__(16) unsigned char buffers[D][kBuffer];
@@ -298,7 +301,7 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
         told = (told + 1) & (kTells - 1);
         more = flags & 2;
         const bool tall = kTall && (flags & 1);
-        const int wm = kLow < 128 ? 0 : tall ? wave >> 1 : wave >> 2, wn = kLow < 128 ? wave : tall ? wave & 1 : wave & 3;
+        const int wm = kLow < 128 ? 0 : tall || kBig ? wave >> 1 : wave >> 2, wn = kLow < 128 ? wave : tall || kBig ? wave & 1 : wave & 3;
         const int x_rows = tall ? kWide : kLow, columns = tall ? kLow : kWide;
         const int x_from = 64 * wm * kXRow, w_from = x_rows * kXRow + (kTurn ? 0 : kColumns * wn * kWRow);
         int turned[kTurn ? FN : 1];  // of columns 16 f of row 8 q + lr / 4
@@ -351,6 +354,41 @@ __global__ __launch_bounds__(64 * (kCopiers + kMultipliers)) void moe_grouped_pr
             auto half = [&](auto which) {
                 constexpr int S = decltype(which)::value;
                 const int piece = 128 * lr + 16 * ((kMxX ? 2 * q + S : 4 * S + q) ^ (lr & 7));
+                if constexpr (kBig) {  // the results take most registers: w's operands come one by one
+                    u32x4 xf[M];
+#pragma unroll
+                    for (int m = 0; m < M; ++m) xf[m] = read16(b, x_from + piece + 2048 * m);
+#pragma unroll
+                    for (int f = 0; f < FN; ++f) {
+                        u32x4 w;
+                        if constexpr (kTurn) {
+                            const u32x2 lo = read_turned(b, turned[f] + 64 * S * columns), hi = read_turned(b, turned[f] + 64 * S * columns + 8 * columns);
+                            w = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                        } else {
+                            w = read16(b, w_from + piece + 2048 * f);
+                        }
+#pragma unroll
+                        for (int m = 0; m < M; ++m) {
+                            if constexpr (kMxX)
+                                acc[f][m] = mfma_mx<S, S>(w, xf[m], acc[f][m], sw[f], sx[m]);
+                            else
+                                acc[f][m] = mfma_bf16(w, xf[m], acc[f][m]);
+                        }
+                    }
+                    if constexpr (F == Form::kRows && M == FM) {
+                        // w's reads three operands ahead of the products: 332 us against 339 with the
+                        // compiler's order (16381 rows of 8 experts by 2816 x 4096); kMx 160 against 121
+                        __builtin_amdgcn_sched_group_barrier(0x100, M + 3, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x8, M, 0);
+#pragma unroll
+                        for (int f = 3; f < FN; ++f) {
+                            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x8, M, 0);
+                        }
+                        __builtin_amdgcn_sched_group_barrier(0x8, 2 * M, 0);
+                    }
+                    return;
+                }
                 u32x4 wf[FN], xf[M];
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
@@ -430,6 +468,16 @@ inline bool read_once(const GroupedArgs& a, int64_t expert_bytes) {
 // 2816: 64 rows in bf16 68 | 79 us, 1024 rows 169 | 168 us, 4096 rows 213 | 174 us; both
 // microscaled 24 | 26, 49 | 50 and 70 | 58 us.
 inline bool low_strips(const GroupedArgs& a) { return a.A <= 8 * static_cast<int64_t>(a.E); }
+
+// Whether tiles of 256 x 256 are faster: strips mostly full, and rounds of tiles mostly full or many.
+// Tiles at most 128 wide | 256 x 256, us: 16381 rows of 8 experts by 2816 x 4096 (748 tiles) bf16 349 | 337,
+// w turned 347 | 335, both microscaled 139 | 121; 16384 rows of 32 experts by 1408 x 2816 (480) 173 |
+// 164, 175 | 166, 68 | 61; 16384 rows of one by 4096 x 4096 (1040) 453 | 429, 459 | 427, 172 | 153.  But 8192
+// rows of 8 by 2816 x 2816 (396) 130 | 150, 132 | 151, 48 | 53, and with 256 rows an expert, 64 by
+// 1408 x 2816, 189 | 224, 185 | 218, 71 | 77.
+inline bool big_tiles(const GroupedArgs& a) {
+    return a.A >= 512 * static_cast<int64_t>(a.E) && (a.A / 256 + a.E / 2) * static_cast<int64_t>((a.N + 255) / 256) >= 448;
+}
 
 }  // namespace
 }  // namespace moe

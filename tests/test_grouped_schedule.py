@@ -93,7 +93,7 @@ CASES = [(16384, 128, 1408), (16381, 8, 2816), (64, 128, 1408), (8, 128, 2816), 
          (700, 1024, 40), (20, 3, 8192), (3000, 2, 72)]
 
 
-@pytest.mark.parametrize("bm,tall", [(256, True), (128, False), (32, False)])
+@pytest.mark.parametrize("bm,tall", [(256, True), (256, False), (128, False), (32, False)])
 @pytest.mark.parametrize("A,E,N", CASES)
 def test_every_row_and_column_once(A, E, N, bm, tall):
     rng = random.Random(A + E + N + bm)
@@ -126,7 +126,7 @@ def test_every_row_and_column_once(A, E, N, bm, tall):
         assert len(units) == want
 
 
-@pytest.mark.parametrize("bm,tall", [(256, True), (128, False), (32, False)])
+@pytest.mark.parametrize("bm,tall", [(256, True), (256, False), (128, False), (32, False)])
 def test_offsets_that_do_not_rise(bm, tall):
     rng = random.Random(bm)
     for _ in range(60):
@@ -139,7 +139,7 @@ def test_offsets_that_do_not_rise(bm, tall):
                 assert 0 <= e < E and 0 <= row and rows >= 1 and row + rows <= A and 0 <= n0 and cols >= 1 and n0 + cols <= N
 
 
-@pytest.mark.parametrize("D", [3, 4])
+@pytest.mark.parametrize("D", [2, 3, 4])
 def test_buffers_and_tiles_told(D):
     """Copies of the stage D - 1 ahead start after a step's barrier; a tile is told when the last stage of the one
     before it is issued, into one of 8 places, and read after the barrier of its first stage."""

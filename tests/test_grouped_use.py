@@ -278,6 +278,24 @@ def test_scales_at_the_ends(sizes, N, K):
     check(got[~nan], ref[~nan], size[~nan], K)
 
 
+# many rows: 448 tiles of 256 x 256 and more, 512 rows an expert and more
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("form", ["bf16", "transposed", "mx"])
+@pytest.mark.parametrize("sizes,N,K", [([9001, 0, 6970], 2040, 288), ([14000], 2056, 160), ([3, 6000, 0, 5000, 70, 1, 300, 257, 4500], 1784, 1056)])
+def test_many_rows(sizes, N, K, form, out):
+    g = gen(N + K)
+    args, kw, x, w = operands(form, g, sum(sizes), len(sizes), N, K)
+    offsets = offsets_of(sizes)
+    assert sum(sizes) >= 512 * len(sizes) and (sum(sizes) // 256 + len(sizes) // 2) * -(-N // 256) >= 448
+    check(bgq.grouped_matmul(*args, offsets, out_dtype=out, **kw), *product(x, w, offsets), K)
+    if sizes[0] == 9001:  # rows behind the last, offsets that fall
+        given = torch.full((sum(sizes), N), 5.0, dtype=out, device="cuda")
+        bgq.grouped_matmul(*args, offsets_of([9000, 0, 6000]), out=given, **kw)
+        assert bool((given[15000:] == 5).all())
+        falling = torch.tensor([20000, 3, 15000, -4], dtype=torch.int32, device="cuda")
+        assert bool(bgq.grouped_matmul(*args, falling, out=given, **kw).isfinite().all())
+
+
 # few rows: wide columns of workgroups (more than 512 narrow ones), their last one in part
 @pytest.mark.parametrize("out", [BF, F32])
 @pytest.mark.parametrize("form", ["bf16", "mx", "bf16 mx"])
