@@ -22,8 +22,8 @@
 // 180 us for 1.05 GB) and, from 32 rows an expert on, the way from L2 to LDS, since each block of columns
 // brings the strip's rows again (16384 rows of 128 experts by 1408 x 2816: 255 us for 1.15 GB of
 // memory and 1.9 GB of copies; both sides microscaled 88 us); with few experts the rate at which LDS
-// feeds the products (16381 rows of 8 experts by 2816 x 4096: 337 us, 1120 TFLOP/s; microscaled 121 us,
-// 3120 TFLOP/s; a stage's reads and copies take as many cycles of LDS as its products on the matrix units).
+// feeds the products (16381 rows of 8 experts by 2816 x 4096: 337 us, 1120 TFLOP/s; microscaled 119 us,
+// 3180 TFLOP/s; a stage's reads and copies take as many cycles of LDS as its products on the matrix units).
 //
 // A buffer holds rows of 128 bytes of K, those of x first, in pieces of 16 bytes XORed
 // with the row's number so that neither the copies nor the reads meet a bank twice (kCols: w
