@@ -2,6 +2,8 @@
 // then the launches.
 #include <limits.h>
 
+#include <numeric>
+
 #include "moe_internal.h"
 
 namespace {
@@ -10,6 +12,29 @@ bool on(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 
 bool plain_type(int32_t t) { return t == MOE_T_BF16 || t == MOE_T_FP32; }
 // A row stride of an input: 16-byte steps, 32-bit offsets inside a tile.
 bool input_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s <= MOE_GROUPED_MAX_STRIDE; }
+
+// The memory of an operand: `rows` runs of `width` bytes, `stride` bytes from one to the next.
+struct Memory {
+    uintptr_t at;
+    int64_t span;    // from the first byte past the last
+    int64_t width;
+    int64_t stride;  // 0: one run
+};
+Memory memory(const void* p, int64_t rows, int64_t width, int64_t stride) {
+    if (!p || rows < 1) return {0, 0, 0, 0};
+    return {reinterpret_cast<uintptr_t>(p), (rows - 1) * stride + width, width, rows > 1 ? stride : 0};
+}
+Memory memory(const void* p, int64_t bytes) { return memory(p, 1, bytes, 0); }
+
+// Whether two operands share bytes.  Their runs repeat with the strides' common divisor: one operand
+// may lie between the other's rows.
+bool meet(const Memory& a, const Memory& b) {
+    if (a.span == 0 || b.span == 0 || a.at >= b.at + b.span || b.at >= a.at + a.span) return false;
+    const int64_t step = std::gcd(a.stride, b.stride);
+    if (step == 0) return true;  // two runs
+    const int64_t ahead = b.at >= a.at ? static_cast<int64_t>((b.at - a.at) % step) : (step - static_cast<int64_t>((a.at - b.at) % step)) % step;
+    return ahead < a.width || step - ahead < b.width;
+}
 
 moe_status check_sizes(int32_t A, int32_t E, int32_t N, int32_t K, int32_t step) {
     if (A < 0 || A >= 1 << 30 || E < 1 || N < 1 || K < 1 || N % 8 || K % step) return MOE_ERR_SHAPE;
@@ -70,7 +95,12 @@ moe_status check(const moe_mx* q, bool quantize) {
     if (q->stride < row || q->stride % (q->type == MOE_T_FP32 ? 4 : 8) || q->stride > int64_t{1} << 30) return MOE_ERR_SHAPE;
     if (q->R == 0) return MOE_OK;
     if (!q->values || !q->codes || !q->scales) return MOE_ERR_NULL;
-    return on(q->values, 16) && on(q->codes, 16) ? MOE_OK : MOE_ERR_ALIGN;
+    if (!on(q->values, 16) || !on(q->codes, 16)) return MOE_ERR_ALIGN;
+    // either way a thread reads what another may have written by then
+    const int64_t size = q->type == MOE_T_FP32 ? 4 : 2;
+    const Memory values = memory(q->values, q->R, size * row, size * q->stride), codes = memory(q->codes, q->R * q->K / 2),
+                 scales = memory(q->scales, q->R * q->K / 32);
+    return meet(values, codes) || meet(values, scales) || meet(codes, scales) ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 moe::MxArgs mx_args(const moe_mx* q) {

@@ -254,7 +254,7 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
     glu="gelu" or "silu" a row of x holds 2 K values [g | u] and v = act(g) u, the product
     between an expert FFN's two matmuls; else v = x.  x may have strided rows in two
     dimensions.  Returns (codes uint8 [..., K / 2], scales uint8 [..., K / 32]), as
-    grouped_matmul takes them."""
+    grouped_matmul takes them (`codes` and `scales` if given, on none of x's memory)."""
     bgq = _layer._api()
     dev = _device(x, "x")
     shape = tuple(x.shape)
@@ -293,8 +293,8 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
 
 def mx_dequantize(codes, scales, *, out=None, out_dtype=None, stream=None):
     """The values [..., K] that microscaled codes [..., K / 2] and scales [..., K / 32] stand
-    for, bf16 or fp32 (`out`, else allocated in out_dtype, bf16 by default; both hold them
-    exactly)."""
+    for, bf16 or fp32 (`out`, on memory of its own, else allocated in out_dtype, bf16 by default;
+    both hold them exactly)."""
     bgq = _layer._api()
     dev = _device(codes, "codes")
     shape = tuple(codes.shape)

@@ -587,7 +587,8 @@ typedef struct {
 } moe_mx;
 
 /* values -> codes and scales.  values and codes start on 16 bytes.  The values are not
- * written. */
+ * written.  Here and below values, codes and scales share no byte (else
+ * MOE_ERR_UNSUPPORTED). */
 moe_status moe_mx_quantize(const moe_mx* q, void* stream);
 
 /* codes and scales -> values, exact in both types (past their range infinity; the byte 255
