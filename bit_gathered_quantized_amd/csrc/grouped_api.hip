@@ -36,6 +36,17 @@ bool meet(const Memory& a, const Memory& b) {
     return ahead < a.width || step - ahead < b.width;
 }
 
+// The same for w, an expert at a time where the memory of all of them meets it.
+bool meet_weights(const Memory& b, const moe_grouped* g) {
+    const bool kn = g->flags & MOE_G_W_KN;
+    const int64_t rows = kn ? g->K : g->N, width = 2 * static_cast<int64_t>(kn ? g->N : g->K), stride = 2 * g->w_stride;
+    const int64_t expert = 2 * (g->w_expert_stride < int64_t{1} << 48 ? g->w_expert_stride : int64_t{1} << 48);
+    if (!meet(memory(g->w, (g->E - 1) * expert + (rows - 1) * stride + width), b)) return false;
+    for (int e = 0; e < g->E; ++e)
+        if (meet(memory(static_cast<const char*>(g->w) + e * expert, rows, width, stride), b)) return true;
+    return false;
+}
+
 moe_status check_sizes(int32_t A, int32_t E, int32_t N, int32_t K, int32_t step) {
     if (A < 0 || A >= 1 << 30 || E < 1 || N < 1 || K < 1 || N % 8 || K % step) return MOE_ERR_SHAPE;
     if (E > MOE_MAX_EXPERTS || N > MOE_GROUPED_MAX_DIM || K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
@@ -61,7 +72,14 @@ moe_status check(const moe_grouped* g) {
     if (!g->x || !g->w || !g->out || (!g->offsets && g->E > 1) || (xm && !g->x_scales) || (wm && !g->w_scales))
         return MOE_ERR_NULL;
     if (!on(g->x, 16) || !on(g->w, 16) || !on(g->out, 16) || !on(g->offsets, 4)) return MOE_ERR_ALIGN;
-    return g->out == g->x || g->out == g->w ? MOE_ERR_UNSUPPORTED : MOE_OK;
+    const int64_t A = g->A, K = g->K, size = g->out_type == MOE_T_FP32 ? 4 : 2, weights = static_cast<int64_t>(g->E) * g->N;
+    const Memory out = memory(g->out, A, size * g->N, size * g->out_stride);
+    if (meet(out, xm ? memory(g->x, A * K / 2) : memory(g->x, A, 2 * K, 2 * g->x_stride)) ||
+        (wm ? meet(out, memory(g->w, weights * K / 2)) : meet_weights(out, g)) ||
+        (xm && meet(out, memory(g->x_scales, A * K / 32))) || (wm && meet(out, memory(g->w_scales, weights * K / 32))) ||
+        meet(out, memory(g->offsets, 4 * (static_cast<int64_t>(g->E) + 1))))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
 }
 
 // Sizes of a gradient of the weights: what the workspace depends on.
@@ -80,7 +98,19 @@ moe_status check(const moe_grouped_grad* g) {
     // without rows dw is zeros all the same
     if (!g->dw || (!g->offsets && g->E > 1) || (g->A > 0 && (!g->dy || !g->x))) return MOE_ERR_NULL;
     if (!on(g->dy, 16) || !on(g->x, 16) || !on(g->dw, 16) || !on(g->offsets, 4)) return MOE_ERR_ALIGN;
-    return g->dw == g->dy || g->dw == g->x ? MOE_ERR_UNSUPPORTED : MOE_OK;
+    return MOE_OK;
+}
+
+// Whether dw or the workspace (`ws_bytes` that the call uses) lies on an operand or on the other.
+bool overlaps(const moe_grouped_grad* g, const void* ws, size_t ws_bytes) {
+    const int64_t N = g->N, K = g->K;
+    const Memory dw = memory(g->dw, (g->out_type == MOE_T_FP32 ? 4 : 2) * g->E * N * K);
+    const Memory space = memory(ws_bytes > 0 ? ws : nullptr, static_cast<int64_t>(ws_bytes));
+    const Memory inputs[] = {memory(g->dy, g->A, 2 * N, 2 * g->dy_stride), memory(g->x, g->A, 2 * K, 2 * g->x_stride),
+                             memory(g->offsets, 4 * (static_cast<int64_t>(g->E) + 1))};
+    for (const Memory& m : inputs)
+        if (meet(dw, m) || meet(space, m)) return true;
+    return meet(dw, space);
 }
 
 moe_status check(const moe_mx* q, bool quantize) {
@@ -158,6 +188,7 @@ moe_status moe_grouped_matmul_dw(const moe_grouped_grad* g, void* ws, size_t ws_
     const size_t need = moe::grouped_dw_workspace(g->A, g->E, g->N, g->K);
     if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
     if (need > 0 && !on(ws, 256)) return MOE_ERR_ALIGN;
+    if (overlaps(g, ws, need)) return MOE_ERR_UNSUPPORTED;
     moe::GroupedGradArgs a = {};
     a.A = g->A;
     a.E = g->E;

@@ -106,8 +106,9 @@ def grouped_matmul(x, w, offsets=None, *, x_scales=None, w_scales=None, transpos
     [E, N, K / 2] with w_scales [E, N, K / 32] (mx_quantize of the weights, K a multiple of
     32), and x bf16, or microscaled too with x_scales.  Products are exact, sums fp32.
 
-    out [A, N] is bf16 or fp32 (`out`, else allocated in out_dtype, bf16 by default).  Rows
-    that belong to no expert are not written.  Returns out."""
+    out [A, N] is bf16 or fp32 (`out`, whose rows share no memory with an input, else allocated
+    in out_dtype, bf16 by default).  Rows that belong to no expert are not written.  Returns
+    out."""
     bgq = _layer._api()
     dev = _device(x, "x")
     xshape, shape = tuple(x.shape), tuple(w.shape)
@@ -180,8 +181,8 @@ def grouped_matmul_dw(dy, x, offsets=None, *, out=None, out_dtype=None, workspac
 
     dy [A, N] and x [A, K] bf16 (rows may be strided), offsets int32 [E + 1]; without
     offsets all rows are one expert's.  N and K are multiples of 8.  Products are exact,
-    sums fp32.  out [E, N, K] is bf16 or fp32 (`out`, contiguous, else allocated in
-    out_dtype, bf16 by default).  workspace: a uint8 tensor of grouped_dw_workspace_bytes(A,
+    sums fp32.  out [E, N, K] is bf16 or fp32 (`out`, contiguous and on memory of its own,
+    else allocated in out_dtype, bf16 by default).  workspace: a uint8 tensor of grouped_dw_workspace_bytes(A,
     E, N, K) bytes, one per call at a time (allocated if None).  Returns out."""
     bgq = _layer._api()
     dev = _device(dy, "dy")

@@ -527,8 +527,9 @@ typedef struct {
     int64_t out_stride;        /* a multiple of 8 (fp32: of 4), >= N, <= MOE_GROUPED_MAX_STRIDE */
 } moe_grouped;
 
-/* x, w and out start on 16 bytes and out lies on none of the inputs.  Deterministic;
- * needs no workspace. */
+/* x, w and out start on 16 bytes, and no row of out shares bytes with an input, offsets
+ * among them (else MOE_ERR_UNSUPPORTED; a row may lie beside one of x or w).
+ * Deterministic; needs no workspace. */
 moe_status moe_grouped_matmul(const moe_grouped* g, void* stream);
 
 /*
@@ -556,6 +557,7 @@ size_t moe_grouped_dw_workspace_bytes(const moe_grouped_grad* g);
 
 /* dy, x and dw start on 16 bytes; ws: moe_grouped_dw_workspace_bytes(g) bytes, 256-byte
  * aligned, with any contents (NULL where that is 0); one call at a time may use it.
+ * dw and ws share no byte with an input or each other (else MOE_ERR_UNSUPPORTED).
  * Deterministic. */
 moe_status moe_grouped_matmul_dw(const moe_grouped_grad* g, void* ws, size_t ws_bytes, void* stream);
 
