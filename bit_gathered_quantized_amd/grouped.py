@@ -5,6 +5,11 @@ in the HIP kernels of ``libmoeffn.so`` and PyTorch supplies memory and streams.
 Everything is enqueued on ``stream`` (default: the current stream of the
 tensors' device); outputs that the caller does not give are allocated for that
 stream.
+
+Autograd does not see these calls.  Where it is on, an input that waits for a gradient
+is refused: a training step calls them under torch.no_grad() or inside a
+torch.autograd.Function, with grouped_matmul(dy, w, transpose=True) and grouped_matmul_dw
+as the backward of grouped_matmul.
 """
 
 from __future__ import annotations
@@ -38,6 +43,13 @@ class MoeGroupedGrad(ctypes.Structure):
 class MoeMx(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int64), ("K", ctypes.c_int32), ("type", ctypes.c_int32), ("flags", ctypes.c_uint32)] + \
                [(n, ctypes.c_void_p) for n in ("values", "codes", "scales")] + [("stride", ctypes.c_int64)]
+
+
+def _no_autograd(*tensors):
+    for t, name in tensors:
+        if t.requires_grad and _layer.torch.is_grad_enabled():
+            raise ValueError(f"{name} waits for a gradient, which this call would not pass on: use torch.no_grad(), detach() or a "
+                             "torch.autograd.Function")
 
 
 def _bytes(t, name, dev, shape, other):
@@ -110,6 +122,8 @@ def grouped_matmul(x, w, offsets=None, *, x_scales=None, w_scales=None, transpos
     in out_dtype, bf16 by default).  Rows that belong to no expert are not written.  Returns
     out."""
     bgq = _layer._api()
+    if x.requires_grad or w.requires_grad:
+        _no_autograd((x, "x"), (w, "w"))
     dev = _device(x, "x")
     xshape, shape = tuple(x.shape), tuple(w.shape)
     if len(xshape) != 2:
@@ -185,6 +199,8 @@ def grouped_matmul_dw(dy, x, offsets=None, *, out=None, out_dtype=None, workspac
     else allocated in out_dtype, bf16 by default).  workspace: a uint8 tensor of grouped_dw_workspace_bytes(A,
     E, N, K) bytes, one per call at a time (allocated if None).  Returns out."""
     bgq = _layer._api()
+    if dy.requires_grad or x.requires_grad:
+        _no_autograd((dy, "dy"), (x, "x"))
     dev = _device(dy, "dy")
     shape, xshape = tuple(dy.shape), tuple(x.shape)
     if len(shape) != 2 or len(xshape) != 2:
@@ -257,6 +273,8 @@ def mx_quantize(x, *, glu=None, codes=None, scales=None, stream=None):
     dimensions.  Returns (codes uint8 [..., K / 2], scales uint8 [..., K / 32]), as
     grouped_matmul takes them (`codes` and `scales` if given, on none of x's memory)."""
     bgq = _layer._api()
+    if x.requires_grad:
+        _no_autograd((x, "x"))
     dev = _device(x, "x")
     shape = tuple(x.shape)
     if len(shape) < 2:
