@@ -120,7 +120,7 @@ moe_status check(const moe_mx* q, bool quantize) {
         return MOE_ERR_UNSUPPORTED;
     if (q->R < 0 || q->K < 1 || q->K % 32) return MOE_ERR_SHAPE;
     if (q->K > MOE_GROUPED_MAX_DIM) return MOE_ERR_UNSUPPORTED;
-    if (q->R >= (int64_t{1} << 34) / q->K) return MOE_ERR_SHAPE;
+    if (q->R > ((int64_t{1} << 34) - 1) / q->K) return MOE_ERR_SHAPE;
     const int64_t row = q->flags ? 2 * static_cast<int64_t>(q->K) : q->K;
     if (q->stride < row || q->stride % (q->type == MOE_T_FP32 ? 4 : 8) || q->stride > int64_t{1} << 30) return MOE_ERR_SHAPE;
     if (q->R == 0) return MOE_OK;

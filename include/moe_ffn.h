@@ -499,8 +499,8 @@ moe_status moe_layer_forward(const moe_problem* p, const moe_layer* l, const voi
 #define MOE_GROUPED_MAX_STRIDE (1 << 22)
 #define MOE_GROUPED_MAX_DIM (1 << 20)
 typedef struct {
-    int32_t A;                 /* rows, 0 <= A < 2^30; (A / 128 + E) (N / 32) < 2^24,
-                                  with up to 192 rows an expert (A / 32 + E) (N / 32)
+    int32_t A;                 /* rows, 0 <= A < 2^30; (A / 128 + E) ceil(N / 32) < 2^24,
+                                  with up to 192 rows an expert (A / 32 + E) ceil(N / 32)
                                   (else MOE_ERR_SHAPE)                                 */
     int32_t E;                 /* experts, 1 <= E <= MOE_MAX_EXPERTS                   */
     int32_t N;                 /* columns of out: a multiple of 8, <= MOE_GROUPED_MAX_DIM */
@@ -538,8 +538,9 @@ moe_status moe_grouped_matmul(const moe_grouped* g, void* stream);
  * rounded once.
  */
 typedef struct {
-    int32_t A;                 /* as in moe_grouped                                    */
-    int32_t E;
+    int32_t A;                 /* rows, 0 <= A < 2^30                                  */
+    int32_t E;                 /* 1 <= E <= MOE_MAX_EXPERTS; E ceil(N / 64) ceil(K / 64)
+                                  < 2^31 - 1 (else MOE_ERR_SHAPE)                      */
     int32_t N;                 /* columns of dy and K of x: multiples of 8,            */
     int32_t K;                 /* <= MOE_GROUPED_MAX_DIM                               */
     int32_t out_type;          /* MOE_T_BF16 or MOE_T_FP32                             */
@@ -585,7 +586,7 @@ typedef struct {
     uint8_t* codes;            /* [R, K / 2], contiguous                               */
     uint8_t* scales;           /* [R, K / 32], contiguous                              */
     int64_t stride;            /* elements from one row of values to the next, a multiple
-                                  of 8 (fp32: of 4), at least a row                    */
+                                  of 8 (fp32: of 4), at least a row, at most 2^30      */
 } moe_mx;
 
 /* values -> codes and scales.  values and codes start on 16 bytes.  The values are not
