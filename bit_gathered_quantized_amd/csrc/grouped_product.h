@@ -474,14 +474,21 @@ inline bool read_once(const GroupedArgs& a, int64_t expert_bytes) {
 // microscaled 24 | 26, 49 | 50 and 70 | 58 us.
 inline bool low_strips(const GroupedArgs& a) { return a.A <= 8 * static_cast<int64_t>(a.E); }
 
-// Whether tiles of 256 x 256 are faster: strips mostly full, and rounds of tiles mostly full or many.
-// Tiles at most 128 wide | 256 x 256, us: 16381 rows of 8 experts by 2816 x 4096 (748 tiles) bf16 349 | 337,
-// w turned 347 | 335, both microscaled 139 | 121; 16384 rows of 32 experts by 1408 x 2816 (480) 173 |
-// 164, 175 | 166, 68 | 61; 16384 rows of one by 4096 x 4096 (1040) 453 | 429, 459 | 427, 172 | 153.  But 8192
-// rows of 8 by 2816 x 2816 (396) 130 | 150, 132 | 151, 48 | 53, and with 256 rows an expert, 64 by
-// 1408 x 2816, 189 | 224, 185 | 218, 71 | 77.
+// Whether tiles of 256 x 256 are faster: strips mostly full, rounds of tiles mostly full or many, and K long enough that
+// a tile's start and its 256 x 256 results do not count.  Tiles at most 128 wide | 256 x 256, us, bf16 out, then fp32:
+// 16381 rows of 8 experts by 2816 x 4096 (748 tiles) 343 | 330, 362 | 359, w turned 347 | 327, 370 | 345, both
+// microscaled 139 | 119, 161 | 142; 16384 rows of 32 experts by 1408 x 2816 (480) 171 | 162, 186 | 176, w turned 174 |
+// 157, 186 | 172, 67 | 59, 81 | 70; 16384 rows of one by 4096 x 4096 (1040) 443 | 429, 489 | 466, w turned 457 | 429,
+// 491 | 459, 172 | 151, 230 | 198.  But 8192 rows of 8 by 2816 x 2816 (396) 129 | 143, 142 | 159, w turned 130 | 141, 141
+// | 159, 48 | 52, 59 | 61, and with 256 rows an expert, 64 by 1408 x 2816, 185 | 220, 197 | 233, w turned 183 | 211, 196 |
+// 225, 71 | 75, 81 | 86.  Short K, bf16 out: 65536 rows of 16 experts by 1024 x 128, 256, 512, 768: 37 | 46, 53 | 63, 92
+// | 95, 128 | 131; w turned 38 | 43, 55 | 59, 92 | 90, 126 | 125; both microscaled 43 | 38, 34 | 38, 42 | 46, 55 | 55.  16381
+// rows of 8 by 2816 x 64, 256, 512, 768: 26 | 27, 39 | 42, 56 | 58, 77 | 78; w turned 26 | 26, 40 | 38, 57 | 54, 82 | 74;
+// both microscaled 31 | 26, 27 | 27, 32 | 31, 40 | 37.
 inline bool big_tiles(const GroupedArgs& a) {
-    return a.A >= 512 * static_cast<int64_t>(a.E) && (a.A / 256 + a.E / 2) * static_cast<int64_t>((a.N + 255) / 256) >= 448;
+    const int32_t least = a.ws ? 0 : a.w_kn ? 256 : 640;
+    return a.K >= least && a.A >= 512 * static_cast<int64_t>(a.E) &&
+           (a.A / 256 + a.E / 2) * static_cast<int64_t>((a.N + 255) / 256) >= 448;
 }
 
 }  // namespace
