@@ -7,10 +7,14 @@
 // at a tile's end: a wave's memory operations end in order, and with copies and stores in one
 // wave the next stage would wait for the last tile's stores.
 //
-// Bound by writing dw: 16384 rows of 128 experts by 1408 x 2816 take 282 us for 1.15 GB, of it
+// Bound by writing dw: 16384 rows of 128 experts by 1408 x 2816 take 286 us for 1.15 GB, of it
 // 1.0 GB of dw.  The stores alone take 184 us, copies and products without stores 167 us; they
 // overlap in part, since the copies' answers come late while the memory is busy with writes (with
 // every expert reading the same rows, from L2, 249 us).
+//
+// Tiles are dealt by their number, an eighth of them to an XCD, and not by their rows: with few experts, or one that
+// has most rows, the XCD with the longest experts ends last.  Rows even | as mild routing spreads them | as 1 / rank:
+// the case above 248 | 286 | 551 us; 16381 rows of 8 experts by 2816 x 4096 363 | 466 | 893 us (an XCD an expert).
 #include "grouped.h"
 
 namespace moe {
@@ -278,8 +282,10 @@ hipError_t launch_grouped_dw(const GroupedGradArgs& a, hipStream_t s) {
     t.n = (a.N + kTileN - 1) / kTileN;
     t.k = (a.K + kTileK - 1) / kTileK;
     t.splits = splits_of(a.A, a.E, a.N, a.K);
-    // Chunks of up to three blocks where every CU gets eight, else single ones: 1 | 2 | 3 | 4 | 6
-    // blocks at 16384 rows of 128 experts by 1408 x 2816 347 | 298 | 282 | 317 | 298 us.
+    // Chunks of up to three blocks where every CU gets eight, else single ones.  1 | 2 | 3 | 4 blocks, us: 16384 rows of 128
+    // experts by 1408 x 2816 348 | 295 | 288 | 316 (6: 298), by 2048 x 2048 369 | 321 | 288 | 325, by 2816 x 1408 333 |
+    // 315 | 296 | 320; of 64 by 2816 x 4096 635 | 621 | 588 | 586; of 256 by 1024 x 2048 304 | 259 | 221 | 243; 4096 rows of
+    // 128 by 1408 x 2816 207 | 212 | 215 | 196.
     t.chunks = static_cast<int64_t>(t.n) * t.k * a.E >= 256 * 8 * 3 ? (t.n + 2) / 3 : t.n;
     t.count = t.chunks * t.k * a.E * t.splits;
     const dim3 grid(t.count < 256 ? (t.count + 7) / 8 * 8 : 256), block(64 * 12);

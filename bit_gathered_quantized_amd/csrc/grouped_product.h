@@ -78,7 +78,7 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& a, const Tile& t, 
                                            int lr, int q) {
     constexpr int kOut = kF32 ? 4 : 2;
     // Of tiles of 256 x 256 the compiler would keep the addresses through the products, in scratch memory (116 to 240
-    // bytes a lane against 36 to 56; in fp32 some of it was read in every stage).  16381 rows of 8 experts by 2816 x
+    // bytes a lane against 36 to 56; for fp32 up to ten reads and writes of it in every stage, now one at most).  16381 rows of 8 experts by 2816 x
     // 4096, kept | made here: bf16 out 334 | 332 us, w turned 329 | 327, both microscaled 121 | 119; fp32 out 363 |
     // 354, 450 | 355, 191 | 141.
     if constexpr (FN == 8) asm("" : "+v"(lr), "+v"(q));
@@ -461,10 +461,13 @@ void launch_product(const GroupedArgs& a, bool once, hipStream_t s) {
     once ? launch_product<F, kLow, true>(a, s) : launch_product<F, kLow, false>(a, s);
 }
 
-// Whether w's rows pass the GPU once and are more than its caches keep (256 MB behind the L2s):
-// then non-temporal loads are faster, 188 | 174 us for 4096 rows of 128 experts by 1408 x 2816 in bf16.
-// Where strips share weights they are slower (16381 rows of 8 experts by 2816 x 4096, 340 |
-// 362 us), and for 8 rows of 2816 x 704, whose 32 MB stay in a cache (11.1 | 12.6 us).
+// Whether w's rows pass the GPU once and come from memory: then non-temporal loads are faster, 188 | 174 us for
+// 4096 rows of 128 experts by 1408 x 2816 in bf16.  Where strips share weights they are slower (16381 rows of 8
+// experts by 2816 x 4096, 340 | 362 us), and for 8 rows of 2816 x 704, whose 32 MB stay in a cache (11.1 | 12.6 us).
+// From 128 MB to the 256 MB that the cache behind the L2s holds it depends on what ran since the last call with them.
+// The next layer's weights push them out (three sets in turn): 72 rows of 18 experts by 1408 x 2816 (143 MB) 30 | 27 us,
+// 512 rows of 32 (254 MB) 49 | 44, codes of 120 experts with 480 bf16 rows (253 MB) 55 | 50.  One set again and again: 24
+// | 26, 41 | 44, 41 | 46.  A model has many layers, so the first is what counts.
 inline bool read_once(const GroupedArgs& a, int64_t expert_bytes) {
     return a.A <= 192 * static_cast<int64_t>(a.E) && (a.A < a.E ? a.A : a.E) * expert_bytes > 128 << 20;
 }

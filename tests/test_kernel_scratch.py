@@ -1,5 +1,5 @@
-"""Scratch memory of the kernels of the grouped products, as the compiler notes it in the built library.  A register that
-goes to scratch is read again in the innermost loop."""
+"""Scratch memory of the kernels of the grouped products, as the compiler notes it in the built library: values that
+its loops would read again from memory."""
 import os
 import struct
 
